@@ -22,7 +22,8 @@ import torch
 from . import _lib
 from ._lib import KdaError
 
-__all__ = ["kda_fwd", "kda_bwd", "kda_step", "fwd_args", "bwd_args", "KdaError", "library"]
+__all__ = ["kda_fwd", "kda_bwd", "kda_step", "fwd_args", "bwd_args", "KdaError", "library", "ssm_fwd", "ssm_step",
+           "draft_verify", "block_norm_fwd", "block_norm_bwd"]
 
 
 def library():
@@ -415,3 +416,220 @@ def kda_step(q, k, v, beta, g, state, accept_len=None, *, scale: float = 1.0, ou
     a = step_args(q, k, v, beta, g, state, acc, o, scale, idx, first, dev_status)
     _lib.check(lib.kda_step(C.byref(a), _stream(q.device)))
     return o
+
+
+# ---------------------------------------------------------------- around the recurrent core
+def _need(t, name, dtype, shape, device):
+    """t as a contiguous CUDA tensor of this dtype and shape, or an exception that names it."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _maybe(t, name, dtype, shape, device):
+    return None if t is None else _need(t, name, dtype, shape, device)
+
+
+def _ints(t, name, n, device):
+    """Optional per-sequence int32 values on ``device`` (converted when they are not)."""
+    if t is None:
+        return None
+    if t.numel() != n:
+        raise ValueError(f"{name} must have one entry per sequence")
+    return t.to(device=device, dtype=torch.int32).contiguous()
+
+
+def _rows(t, name, T, heads, dim, like):
+    """Row stride of a [T, heads, dim] view whose rows are dense."""
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must share x's dtype")
+    if t.shape != (T, heads, dim) or t.device != like.device:
+        raise ValueError(f"{name} must be [{T}, {heads}, {dim}] on {like.device}")
+    if t.numel() == 0:
+        return heads * dim
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}'s rows must be dense (heads and channels side by side)")
+    return t.stride(0) if T > 1 else heads * dim
+
+
+def ssm_fwd(x, dt, a, b, c, cu_seqlens=None, h0=None, *, d_skip=None, dt_bias=None, dt_softplus: bool = True,
+            final_state: bool = True, n_seqs: Optional[int] = None, dev_status=None):
+    """Selective state space scan over packed prompts. Returns (y [T, H, P], hT or None).
+
+    x [T, H, P] (P = 64 or 128), b and c [T, G, 128] in bfloat16 or float32 may be views into one
+    row, such as conv_fwd's output split into [x | B | C]; dt [T, H], a [H], d_skip [H], dt_bias
+    [H] are fp32, and the states h0, hT [N, H, 128, P] fp32 (row = state channel). Per token and
+    head: h = softplus(dt + dt_bias), S = exp(h a) S + h B x^T, y = S^T C + d_skip x.
+    """
+    lib = library()
+    if x.dim() != 3 or not x.is_cuda or b.dim() != 3:
+        raise ValueError("x must be a CUDA tensor [T, H, P] and b [T, G, 128]")
+    dev = x.device
+    (T, H, P), G = x.shape, b.shape[1]
+    cu = _i32(cu_seqlens, dev)
+    N = (cu.numel() - 1) if cu is not None else (n_seqs or 1)
+    f32 = torch.float32
+    s = _lib.SsmArgs()
+    s.n_seqs, s.total_tokens, s.heads, s.groups, s.head_dim, s.d_state = N, T, H, G, P, b.shape[2]
+    s.io_dtype, s.dt_softplus = _io_dtype(x), int(dt_softplus)
+    s.cu_seqlens, s.x, s.b, s.c = _ptr(cu), x.data_ptr(), b.data_ptr(), c.data_ptr()
+    s.ldx, s.ldb, s.ldc = _rows(x, "x", T, H, P, x), _rows(b, "b", T, G, b.shape[2], x), _rows(c, "c", T, G, b.shape[2], x)
+    s.dt, s.a = _need(dt, "dt", f32, (T, H), dev), _need(a, "a", f32, (H,), dev)
+    s.dt_bias, s.d_skip = _maybe(dt_bias, "dt_bias", f32, (H,), dev), _maybe(d_skip, "d_skip", f32, (H,), dev)
+    s.h0 = _maybe(h0, "h0", f32, (N, H, b.shape[2], P), dev)
+    y = torch.empty((T, H, P), dtype=x.dtype, device=dev)
+    hT = torch.empty((N, H, b.shape[2], P), dtype=f32, device=dev) if final_state else None
+    s.y, s.hT, s.dev_status = y.data_ptr(), _ptr(hT), _ptr(dev_status)
+    ws_bytes = lib.kda_ssm_fwd_workspace_size(C.byref(s))
+    if ws_bytes:
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        s.workspace, s.workspace_bytes = ws.data_ptr(), ws_bytes
+    _lib.check(lib.kda_ssm_fwd(C.byref(s), _stream(dev)))
+    return y, hT
+
+
+def ssm_step(xbc, dt, a, conv_weight, conv_bias, conv_state, state, accept_len=None, *, groups: int = 1, d_skip=None,
+             dt_bias=None, dt_softplus: bool = True, activation: str = "silu", state_indices=None, first_slot=None,
+             out=None, dev_status=None):
+    """Decode / verify L token slots per sequence through the short convolution and the
+    selective scan; returns y [N, L, H, P].
+
+    xbc [N, L, C] holds the raw rows [x | B | C], C = H P + 2 groups 128; ``conv_state``
+    [N, W-1, C] (xbc's dtype) and ``state`` [N, H, 128, P] fp32, or pools addressed by
+    ``state_indices`` [N], advance in place through ``accept_len`` slots; slots before
+    ``first_slot`` are padding (their outputs are not written). conv_weight [C, W], conv_bias
+    [C], dt [N, L, H], a, d_skip, dt_bias [H] are fp32.
+    """
+    lib = library()
+    if xbc.dim() != 3 or not xbc.is_cuda or not xbc.is_contiguous() or state.dim() != 4 or conv_weight.dim() != 2:
+        raise ValueError("xbc must be a contiguous CUDA tensor [N, L, C], state [slots, H, 128, P], conv_weight [C, W]")
+    dev, f32 = xbc.device, torch.float32
+    N, L, Cc = xbc.shape
+    slots, H, D, P = state.shape
+    W = conv_weight.shape[1]
+    if Cc != H * P + 2 * groups * D:
+        raise ValueError(f"xbc has {Cc} channels, the heads and groups need {H * P + 2 * groups * D}")
+    acc, idx = _ints(accept_len, "accept_len", N, dev), _ints(state_indices, "state_indices", N, dev)
+    first = _ints(first_slot, "first_slot", N, dev)
+    if idx is None and slots != N:
+        raise ValueError("state has one slot per sequence unless state_indices [N] addresses a pool")
+    s = _lib.SsmStepArgs()
+    s.n_seqs, s.steps, s.heads, s.groups, s.head_dim, s.d_state = N, L, H, groups, P, D
+    s.io_dtype, s.dt_softplus, s.width, s.activation = _io_dtype(xbc), int(dt_softplus), W, _ACT[activation]
+    s.xbc = xbc.data_ptr()
+    s.conv_weight = _need(conv_weight, "conv_weight", f32, (Cc, W), dev)
+    s.conv_bias = _maybe(conv_bias, "conv_bias", f32, (Cc,), dev)
+    if W > 1:
+        s.conv_state = _need(conv_state, "conv_state", xbc.dtype, (slots, W - 1, Cc), dev)
+    s.dt, s.a = _need(dt, "dt", f32, (N, L, H), dev), _need(a, "a", f32, (H,), dev)
+    s.dt_bias, s.d_skip = _maybe(dt_bias, "dt_bias", f32, (H,), dev), _maybe(d_skip, "d_skip", f32, (H,), dev)
+    s.state = _need(state, "state", f32, (slots, H, D, P), dev)
+    s.state_indices, s.accept_len, s.first_slot, s.n_slots = _ptr(idx), _ptr(acc), _ptr(first), slots
+    y = torch.empty((N, L, H, P), dtype=xbc.dtype, device=dev) if out is None else out
+    s.y, s.dev_status = _need(y, "out", xbc.dtype, (N, L, H, P), dev), _ptr(dev_status)
+    ws_bytes = lib.kda_ssm_step_workspace_size(C.byref(s))
+    ws = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
+    s.workspace, s.workspace_bytes = ws.data_ptr(), ws_bytes
+    _lib.check(lib.kda_ssm_step(C.byref(s), _stream(dev)))
+    return y
+
+
+def draft_verify(p, q, draft, u, noise, draft_len=None):
+    """Speculative sampling from given random numbers: how many drafted tokens stand and which
+    token follows. Returns int32 (accept_len [N], first_slot [N] = L - accept_len, tokens
+    [N, L+1]: the accepted drafts, the next token, then -1).
+
+    p [N, L+1, V] are the target's probabilities, q [N, L, V] the drafter's in the same dtype
+    (bfloat16 or float32; None: the drafter is certain of its draft); draft [N, L] int32, u
+    [N, L] fp32 uniforms in [0, 1), noise [N, V] fp32 Exp(1) variates, draft_len [N] optional
+    lengths. Draft j stands while u q(x) < p(x); the next token wins the race r / noise over
+    r = max(p - q, 0) after a rejection, r = p after the last draft (see include/kda.h).
+    accept_len and first_slot go straight into kda_step / conv_step / ssm_step.
+    """
+    lib = library()
+    if p.dim() != 3 or not p.is_cuda:
+        raise ValueError("p must be a CUDA tensor [N, L+1, V]")
+    dev, f32, i32 = p.device, torch.float32, torch.int32
+    N, L, V = p.shape[0], p.shape[1] - 1, p.shape[2]
+    s = _lib.DraftVerifyArgs()
+    s.n_seqs, s.drafts, s.vocab, s.io_dtype = N, L, V, _io_dtype(p)
+    s.p, s.q = _need(p, "p", p.dtype, (N, L + 1, V), dev), _maybe(q, "q", p.dtype, (N, L, V), dev)
+    s.draft, s.u = _need(draft, "draft", i32, (N, L), dev), _need(u, "u", f32, (N, L), dev)
+    s.noise = _need(noise, "noise", f32, (N, V), dev)
+    lens = _ints(draft_len, "draft_len", N, dev)
+    s.draft_len = _ptr(lens)
+    accept, first = torch.empty(N, dtype=i32, device=dev), torch.empty(N, dtype=i32, device=dev)
+    tokens = torch.empty((N, L + 1), dtype=i32, device=dev)
+    s.accept_len, s.first_slot, s.tokens = accept.data_ptr(), first.data_ptr(), tokens.data_ptr()
+    _lib.check(lib.kda_draft_verify(C.byref(s), _stream(dev)))
+    return accept, first, tokens
+
+
+_GATE = {"sigmoid": _lib.KDA_GATE_SIGMOID, "silu": _lib.KDA_GATE_SILU}
+
+
+def _block_norm_args(u, w_post, gate, gate_act, residual, scale, w_pre, eps):
+    if u.dim() < 1 or not u.is_cuda or not u.is_contiguous():
+        raise ValueError("u must be a contiguous CUDA tensor [..., d]")
+    dev, d, f32 = u.device, u.shape[-1], torch.float32
+    n = _lib.BlockNormArgs()
+    n.rows, n.dim, n.eps, n.io_dtype = (u.numel() // d if d else 0), d, eps, _io_dtype(u)
+    n.gate_act = _GATE[gate_act]
+    n.u = u.data_ptr()
+    n.gate = _maybe(gate, "gate", u.dtype, u.shape, dev)
+    n.residual = _maybe(residual, "residual", u.dtype, u.shape, dev)
+    n.w_post, n.scale = _maybe(w_post, "w_post", f32, (d,), dev), _maybe(scale, "scale", f32, (d,), dev)
+    n.w_pre = _maybe(w_pre, "w_pre", f32, (d,), dev)
+    return n
+
+
+def block_norm_fwd(u, w_post, *, gate=None, gate_act: str = "silu", residual=None, scale=None, w_pre=None,
+                   eps: float = 1e-6):
+    """The norm after a block, its gate and residual scale, the residual sum and the norm before
+    the next block, over rows u [..., d]:
+
+        out = residual + scale * (w_post * rms_norm(u) * act(gate)),  normed = w_pre * rms_norm(out)
+
+    w_post None leaves u as it is; gate, residual, scale and w_pre are optional. Returns (out,
+    normed or None, stats); stats = (rstd_post, rstd_pre), fp32 [rows] or None, go to
+    block_norm_bwd. With u the [T, H, d] output of the recurrent core this is its per-head
+    output norm.
+    """
+    lib = library()
+    n = _block_norm_args(u, w_post, gate, gate_act, residual, scale, w_pre, eps)
+    out = torch.empty_like(u)
+    normed = torch.empty_like(u) if w_pre is not None else None
+    rstd = lambda on: torch.empty(n.rows, dtype=torch.float32, device=u.device) if on is not None else None
+    stats = (rstd(w_post), rstd(w_pre))
+    n.out, n.normed, n.rstd_post, n.rstd_pre = out.data_ptr(), _ptr(normed), _ptr(stats[0]), _ptr(stats[1])
+    _lib.check(lib.kda_block_norm_fwd(C.byref(n), _stream(u.device)))
+    return out, normed, stats
+
+
+def block_norm_bwd(u, w_post, stats, d_out, d_normed=None, *, gate=None, gate_act: str = "silu", residual=None,
+                   scale=None, w_pre=None, eps: float = 1e-6, dev_status=None):
+    """Backward of block_norm_fwd (``stats`` from it, the same inputs). d_out and d_normed are the
+    gradients of its two results, None for zero. Returns a dict: du, dgate, dresidual in u's
+    dtype and dw_post, dscale, dw_pre fp32 [d], None where the input was absent."""
+    lib = library()
+    dev, f32 = u.device, torch.float32
+    b = _lib.BlockNormBwdArgs()
+    b.fwd = _block_norm_args(u, w_post, gate, gate_act, residual, scale, w_pre, eps)
+    rows, d = b.fwd.rows, b.fwd.dim
+    for i, (name, w) in enumerate((("rstd_post", w_post), ("rstd_pre", w_pre))):
+        if w is not None:
+            setattr(b.fwd, name, _need(stats[i], name, f32, (rows,), dev))
+    b.d_out, b.d_normed = _maybe(d_out, "d_out", u.dtype, u.shape, dev), _maybe(d_normed, "d_normed", u.dtype, u.shape, dev)
+    like = lambda t: None if t is None else torch.empty_like(u)
+    vec = lambda t: None if t is None else torch.empty(d, dtype=f32, device=dev)
+    g = {"du": torch.empty_like(u), "dgate": like(gate), "dresidual": like(residual), "dw_post": vec(w_post),
+         "dscale": vec(scale), "dw_pre": vec(w_pre)}
+    b.du, b.d_gate, b.d_residual = _ptr(g["du"]), _ptr(g["dgate"]), _ptr(g["dresidual"])
+    b.dw_post, b.dscale, b.dw_pre, b.dev_status = _ptr(g["dw_post"]), _ptr(g["dscale"]), _ptr(g["dw_pre"]), _ptr(dev_status)
+    ws_bytes = lib.kda_block_norm_bwd_workspace_size(C.byref(b))
+    ws = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
+    b.workspace, b.workspace_bytes = ws.data_ptr(), ws_bytes
+    _lib.check(lib.kda_block_norm_bwd(C.byref(b), _stream(dev)))
+    return g

@@ -20,10 +20,13 @@ ABI_VERSION = 5
 EXPORTS = ("kda_fwd", "kda_fwd_workspace_size", "kda_saved_size", "kda_bwd", "kda_bwd_workspace_size",
            "kda_step", "kda_cp_combine", "kda_fwd_cp", "kda_fwd_cp_workspace_size", "kda_attnres_fwd", "kda_attnres_bwd", "kda_attnres_bwd_workspace_size",
            "kda_conv_fwd", "kda_conv_bwd", "kda_conv_bwd_workspace_size", "kda_conv_step",
+           "kda_ssm_fwd", "kda_ssm_fwd_workspace_size", "kda_ssm_step", "kda_ssm_step_workspace_size",
+           "kda_draft_verify", "kda_block_norm_fwd", "kda_block_norm_bwd", "kda_block_norm_bwd_workspace_size",
            "kda_fwd_no_alloc", "kda_set_profile_events", "kda_last_error", "kda_abi_version")
 ATTNRES_MAX_SOURCES = 9
 CONV_MAX_WIDTH = 4
 KDA_ACT_NONE, KDA_ACT_SILU = 0, 1
+KDA_GATE_SIGMOID, KDA_GATE_SILU = 0, 1
 NO_ALLOC_SCRATCH_BYTES = 256 * 1024 * 1024
 
 
@@ -94,6 +97,54 @@ class ConvStepArgs(C.Structure):
     ]
 
 
+class SsmArgs(C.Structure):
+    _fields_ = [
+        ("n_seqs", C.c_int32), ("total_tokens", C.c_int64), ("heads", C.c_int32), ("groups", C.c_int32),
+        ("head_dim", C.c_int32), ("d_state", C.c_int32), ("io_dtype", C.c_int32), ("dt_softplus", C.c_int32),
+        ("cu_seqlens", C.c_void_p), ("x", C.c_void_p), ("b", C.c_void_p), ("c", C.c_void_p),
+        ("ldx", C.c_int64), ("ldb", C.c_int64), ("ldc", C.c_int64), ("dt", C.c_void_p), ("a", C.c_void_p),
+        ("dt_bias", C.c_void_p), ("d_skip", C.c_void_p), ("h0", C.c_void_p), ("y", C.c_void_p), ("hT", C.c_void_p),
+        ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t), ("dev_status", C.c_void_p),
+    ]
+
+
+class SsmStepArgs(C.Structure):
+    _fields_ = [
+        ("n_seqs", C.c_int32), ("steps", C.c_int32), ("heads", C.c_int32), ("groups", C.c_int32),
+        ("head_dim", C.c_int32), ("d_state", C.c_int32), ("io_dtype", C.c_int32), ("dt_softplus", C.c_int32),
+        ("width", C.c_int32), ("activation", C.c_int32), ("xbc", C.c_void_p), ("conv_weight", C.c_void_p),
+        ("conv_bias", C.c_void_p), ("conv_state", C.c_void_p), ("dt", C.c_void_p), ("a", C.c_void_p),
+        ("dt_bias", C.c_void_p), ("d_skip", C.c_void_p), ("state", C.c_void_p), ("state_indices", C.c_void_p),
+        ("accept_len", C.c_void_p), ("first_slot", C.c_void_p), ("n_slots", C.c_int32), ("y", C.c_void_p),
+        ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t), ("dev_status", C.c_void_p),
+    ]
+
+
+class DraftVerifyArgs(C.Structure):
+    _fields_ = [
+        ("n_seqs", C.c_int32), ("drafts", C.c_int32), ("vocab", C.c_int32), ("io_dtype", C.c_int32),
+        ("p", C.c_void_p), ("q", C.c_void_p), ("draft", C.c_void_p), ("draft_len", C.c_void_p), ("u", C.c_void_p),
+        ("noise", C.c_void_p), ("accept_len", C.c_void_p), ("first_slot", C.c_void_p), ("tokens", C.c_void_p),
+    ]
+
+
+class BlockNormArgs(C.Structure):
+    _fields_ = [
+        ("rows", C.c_int64), ("dim", C.c_int32), ("eps", C.c_float), ("io_dtype", C.c_int32), ("gate_act", C.c_int32),
+        ("u", C.c_void_p), ("gate", C.c_void_p), ("residual", C.c_void_p), ("w_post", C.c_void_p), ("scale", C.c_void_p),
+        ("w_pre", C.c_void_p), ("out", C.c_void_p), ("normed", C.c_void_p), ("rstd_post", C.c_void_p),
+        ("rstd_pre", C.c_void_p),
+    ]
+
+
+class BlockNormBwdArgs(C.Structure):
+    _fields_ = [
+        ("fwd", BlockNormArgs), ("d_out", C.c_void_p), ("d_normed", C.c_void_p), ("du", C.c_void_p),
+        ("d_gate", C.c_void_p), ("d_residual", C.c_void_p), ("dw_post", C.c_void_p), ("dscale", C.c_void_p),
+        ("dw_pre", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t), ("dev_status", C.c_void_p),
+    ]
+
+
 class BwdArgs(C.Structure):
     _fields_ = [
         ("fwd", FwdArgs), ("dO", C.c_void_p), ("dhT", C.c_void_p),
@@ -157,6 +208,16 @@ def load(path: str = LIB_PATH):
     lib.kda_conv_bwd_workspace_size.restype = C.c_size_t
     lib.kda_conv_step.argtypes = [C.POINTER(ConvStepArgs), C.c_void_p]
     lib.kda_conv_step.restype = C.c_int
+    for name, args, restype in (("kda_ssm_fwd", SsmArgs, C.c_int), ("kda_ssm_fwd_workspace_size", SsmArgs, C.c_size_t),
+                                ("kda_ssm_step", SsmStepArgs, C.c_int),
+                                ("kda_ssm_step_workspace_size", SsmStepArgs, C.c_size_t),
+                                ("kda_draft_verify", DraftVerifyArgs, C.c_int),
+                                ("kda_block_norm_fwd", BlockNormArgs, C.c_int),
+                                ("kda_block_norm_bwd", BlockNormBwdArgs, C.c_int),
+                                ("kda_block_norm_bwd_workspace_size", BlockNormBwdArgs, C.c_size_t)):
+        fn = getattr(lib, name)
+        fn.argtypes = [C.POINTER(args)] + ([C.c_void_p] if restype is C.c_int else [])
+        fn.restype = restype
     lib.kda_fwd_workspace_size.argtypes = [C.POINTER(FwdArgs)]
     lib.kda_fwd_workspace_size.restype = C.c_size_t
     lib.kda_saved_size.argtypes = [C.POINTER(FwdArgs)]

@@ -219,6 +219,63 @@ cudaError_t launch_cp_segments(const int *cu, int n_seqs, long long total, int P
 // hT[n] = hseg[n * P + P - 1] for the N sequences ([N][H][128][128] fp32 each)
 cudaError_t launch_cp_last(const float *hseg, int n_seqs, int P, int heads, float *hT, cudaStream_t s);
 
+// Selective state space scan. Prompts (kda_ssm.cu, kda_ssm_tc.cu): x, b, c with row strides, cu
+// offsets, h0 -> y, hT. Step: the raw rows go through ssm_conv_step into `conv` (fp32
+// [N][L][C]), and the scan reads x, B and C from there; the pools advance in place.
+constexpr int SSM_N = 128;     // d_state
+constexpr int SSM_COLS = 64;   // value columns per CTA: a head of 128 takes two
+struct SsmParams {
+  int n_seqs, H, G, P;
+  long long T;
+  int softplus;
+  const int *cu;
+  const void *x, *b, *c;
+  long long ldx, ldb, ldc;
+  const float *dt, *a, *dt_bias, *d_skip, *h0;
+  void *y;
+  float *hT;
+  int *status;
+  // step
+  int L, n_slots, W, act;
+  const void *xbc;
+  const float *cw, *cbias;
+  void *conv_state;
+  float *conv;
+  float *state;
+  const int *idx, *acc, *first;
+};
+cudaError_t launch_ssm_fwd_rec(const SsmParams &p, bool f32, cudaStream_t s);
+cudaError_t launch_ssm_step(const SsmParams &p, bool f32, cudaStream_t s);
+
+// Draft verification (kda_verify.cu).
+struct VerifyParams {
+  int n_seqs, L, V;
+  const void *p, *q;
+  const int *draft, *draft_len;
+  const float *u, *noise;
+  int *accept, *first, *tokens;
+};
+cudaError_t launch_draft_verify(const VerifyParams &p, bool f32, cudaStream_t s);
+
+// Block norm (kda_block_norm.cu). Absent parts are null.
+struct BlockNormParams {
+  long long rows;
+  int dim, silu;
+  float eps, inv_dim;
+  const void *u, *gate, *residual;
+  const float *w_post, *scale, *w_pre;
+  void *out, *normed;
+  float *rstd_post, *rstd_pre;
+  const void *d_out, *d_normed;
+  void *du, *d_gate, *d_residual;
+  float *dw_post, *dscale, *dw_pre;
+  float *partial;              // [backward CTAs][2][dim]
+  int *status;
+};
+cudaError_t launch_block_norm_fwd(const BlockNormParams &p, bool f32, cudaStream_t s);
+cudaError_t launch_block_norm_bwd(const BlockNormParams &p, bool f32, cudaStream_t s);
+int block_norm_bwd_ctas(long long rows, int dim, bool f32);
+
 // Sets the message that kda_last_error() returns on this host thread.
 void set_last_error(const char *msg);
 

@@ -369,6 +369,161 @@ size_t kda_conv_bwd_workspace_size(const kda_conv_bwd_args *args);
 kda_status kda_conv_step(const kda_conv_step_args *args, cudaStream_t stream);
 
 /*
+ * Selective state space scan: a recurrent mixer beside KDA with the same packing, state and
+ * decode conventions. Per sequence and head, with the fp32 state S of shape [d_state][head_dim]
+ * (row n = state channel, column p = value channel), one scalar decay per head and token:
+ *     h_t = softplus(dt_t + dt_bias)   (or dt_t + dt_bias without dt_softplus)
+ *     S_t = exp(h_t a) S_{t-1} + h_t B_t x_t^T,      y_t = S_t^T C_t + d_skip x_t
+ * B and C are shared by the heads / groups consecutive heads of a group. x, B and C are
+ * usually the output of kda_conv_fwd, side by side in one row of H * head_dim +
+ * 2 * groups * d_state channels, and are read in place through their row strides.
+ *  - d_state = 128; head_dim 64 or 128; groups divides heads; a <= 0 is expected.
+ *  - Row strides (ld*, in elements) must be multiples of 8 and at least the row's width.
+ *  - Inputs are finite. A sequence's outputs depend on that sequence's rows only.
+ * bf16 I/O: the products run on the tensor cores in chunks of 128 tokens; the state, the
+ * decays and all sums are fp32. The state update splits its fp32 factor into three bf16 terms
+ * (error 2^-24 of a term). The decay-weighted scores of a chunk are rounded to bf16 once before
+ * their product with x, which costs y about as much as its own rounding to bf16. fp32 I/O runs
+ * in fp32 on the CUDA cores.
+ */
+typedef struct {
+    int32_t n_seqs;            /* N >= 0                                                 */
+    int64_t total_tokens;      /* T, < 2^31                                              */
+    int32_t heads, groups;     /* H, G                                                   */
+    int32_t head_dim, d_state; /* 64 or 128; 128                                         */
+    int32_t io_dtype;          /* kda_dtype of x, b, c, y                                */
+    int32_t dt_softplus;       /* nonzero: h = softplus(dt + dt_bias)                    */
+    const int32_t *cu_seqlens; /* [N+1] or NULL: N sequences of equal length T/N         */
+    const void *x;             /* [T, H, head_dim], row stride ldx                       */
+    const void *b, *c;         /* [T, G, d_state], row strides ldb, ldc                  */
+    int64_t ldx, ldb, ldc;     /* elements between rows                                  */
+    const float *dt;           /* [T, H]                                                 */
+    const float *a;            /* [H]                                                    */
+    const float *dt_bias;      /* [H] or NULL (zero)                                     */
+    const float *d_skip;       /* [H] or NULL (zero)                                     */
+    const float *h0;           /* [N, H, d_state, head_dim] or NULL (zero)               */
+    void *y;                   /* out [T, H, head_dim]                                   */
+    float *hT;                 /* out [N, H, d_state, head_dim] or NULL                   */
+    void *workspace;           /* kda_ssm_fwd_workspace_size() bytes (0: may be NULL)    */
+    size_t workspace_bytes;
+    int32_t *dev_status;       /* optional device int32, as in kda_fwd_args              */
+} kda_ssm_args;
+
+kda_status kda_ssm_fwd(const kda_ssm_args *args, cudaStream_t stream);
+size_t kda_ssm_fwd_workspace_size(const kda_ssm_args *args);
+
+/* Decode / draft verification of the selective scan behind its short convolution: L raw token
+ * slots per sequence, [x | B | C] side by side before the convolution, with the slot
+ * conventions of kda_step and kda_conv_step (state_indices into pools of n_slots states; slots
+ * before first_slot[i] are padding; both states advance through accept_len[i] slots). The
+ * convolution's outputs stay in fp32 between the two. */
+typedef struct {
+    int32_t n_seqs, steps;     /* N in 0..65535, L in 1..8                               */
+    int32_t heads, groups, head_dim, d_state;   /* as in kda_ssm_args                    */
+    int32_t io_dtype, dt_softplus;
+    int32_t width, activation; /* the convolution: 1..KDA_CONV_MAX_WIDTH, kda_activation */
+    const void *xbc;           /* [N, L, C], C = H * head_dim + 2 * G * d_state          */
+    const float *conv_weight;  /* [C, W]                                                 */
+    const float *conv_bias;    /* [C] or NULL                                            */
+    void *conv_state;          /* [n_slots, W-1, C] io dtype, updated in place           */
+    const float *dt;           /* [N, L, H]                                              */
+    const float *a, *dt_bias, *d_skip;   /* [H]; the last two may be NULL                */
+    float *state;              /* [n_slots, H, d_state, head_dim], updated in place      */
+    const int32_t *state_indices, *accept_len, *first_slot;   /* [N] or NULL, as above   */
+    int32_t n_slots;           /* slots of both pools (N when state_indices is NULL)     */
+    void *y;                   /* out [N, L, H, head_dim]; padding slots are not written */
+    void *workspace;           /* kda_ssm_step_workspace_size() bytes                    */
+    size_t workspace_bytes;
+    int32_t *dev_status;       /* KDA_ERR_INVALID_ARG for a slot outside 0..n_slots-1
+                                  (that sequence is skipped)                             */
+} kda_ssm_step_args;
+
+kda_status kda_ssm_step(const kda_ssm_step_args *args, cudaStream_t stream);
+size_t kda_ssm_step_workspace_size(const kda_ssm_step_args *args);
+
+/*
+ * Draft verification (speculative sampling): decides how many of each sequence's drafted
+ * tokens stand, and draws the token that follows them, from given random numbers. Position j
+ * of sequence i holds the target's probabilities p[i, j, :] after j accepted drafts.
+ *  - Draft j is accepted while u[i, j] * q[i, j, x_j] < p[i, j, x_j], x_j = draft[i, j]
+ *    (q NULL: the drafter is certain, q = 1 at the draft). The drafts of a sequence end at
+ *    draft_len[i], or at the first token outside 0..V-1.
+ *  - With a = the number accepted: the next token maximises r_v / noise[i, v] over v, the
+ *    lowest index on a tie, with r = max(p[i, a] - q[i, a], 0) after a rejection and r = p[i, a]
+ *    when every draft stood. noise holds Exp(1) variates, which makes this a draw from r / sum r.
+ *    Entries that are not positive, or NaN, never win; if none of r is positive, p[i, a] takes
+ *    its place, and if none of p[i, a] is positive either, the token is -1.
+ * accept_len feeds kda_step / kda_conv_step / kda_ssm_step directly: a replay window of
+ * L slots with first_slot = L - accept_len. tokens[i] holds the accepted drafts, the next
+ * token, then -1.
+ */
+typedef struct {
+    int32_t n_seqs, drafts;    /* N in 0..65535, L in 1..8                               */
+    int32_t vocab;             /* V >= 1                                                 */
+    int32_t io_dtype;          /* kda_dtype of p and q                                   */
+    const void *p;             /* [N, L+1, V]                                            */
+    const void *q;             /* [N, L, V] or NULL                                      */
+    const int32_t *draft;      /* [N, L]                                                 */
+    const int32_t *draft_len;  /* [N] (clamped to 0..L) or NULL (L)                      */
+    const float *u;            /* [N, L] uniforms in [0, 1)                              */
+    const float *noise;        /* [N, V] Exp(1) variates                                 */
+    int32_t *accept_len;       /* out [N]                                                */
+    int32_t *first_slot;       /* out [N]: L - accept_len, or NULL                       */
+    int32_t *tokens;           /* out [N, L+1]                                           */
+} kda_draft_verify_args;
+
+kda_status kda_draft_verify(const kda_draft_verify_args *args, cudaStream_t stream);
+
+/*
+ * Block norm: the norm after a block, its gate and residual scale, the residual sum, and the
+ * norm before the next block, in one pass over each row of d elements:
+ *     m    = w_post u / sqrt(mean(u^2) + eps)       (w_post NULL: m = u)
+ *     m   *= act(gate)                              (gate optional: sigmoid or SiLU)
+ *     out  = residual + scale m                     (residual, scale optional)
+ *     normed = w_pre out / sqrt(mean(out^2) + eps)  (w_pre optional)
+ * normed is formed from the unrounded out. Rows are tokens, or (token, head) pairs for the
+ * output norm of a recurrent core.
+ */
+typedef enum { KDA_GATE_SIGMOID = 0, KDA_GATE_SILU = 1 } kda_gate;
+
+typedef struct {
+    int64_t rows;              /* R >= 0, < 2^31                                         */
+    int32_t dim;               /* d, a multiple of 8 in 8..16384                         */
+    float eps;                 /* > 0                                                    */
+    int32_t io_dtype;          /* kda_dtype of u, gate, residual, out, normed, gradients */
+    int32_t gate_act;          /* kda_gate                                               */
+    const void *u;             /* [R, d]                                                 */
+    const void *gate;          /* [R, d] or NULL                                         */
+    const void *residual;      /* [R, d] or NULL                                         */
+    const float *w_post;       /* [d] or NULL                                            */
+    const float *scale;        /* [d] or NULL                                            */
+    const float *w_pre;        /* [d] or NULL                                            */
+    void *out;                 /* out [R, d]                                             */
+    void *normed;              /* out [R, d], with w_pre                                 */
+    float *rstd_post;          /* out [R], with w_post (kept for the backward)           */
+    float *rstd_pre;           /* out [R], with w_pre  (kept for the backward)           */
+} kda_block_norm_args;
+
+typedef struct {
+    kda_block_norm_args fwd;   /* the forward's arguments and statistics (out, normed unused) */
+    const void *d_out;         /* [R, d] gradient of out, or NULL (zero)                 */
+    const void *d_normed;      /* [R, d] gradient of normed, or NULL (zero)              */
+    void *du;                  /* out [R, d]                                             */
+    void *d_gate;              /* out [R, d], with gate                                  */
+    void *d_residual;          /* out [R, d], with residual                              */
+    float *dw_post;            /* out [d], with w_post                                   */
+    float *dscale;             /* out [d], with scale                                    */
+    float *dw_pre;             /* out [d], with w_pre                                    */
+    void *workspace;           /* kda_block_norm_bwd_workspace_size() bytes              */
+    size_t workspace_bytes;
+    int32_t *dev_status;       /* optional device int32, as in kda_fwd_args              */
+} kda_block_norm_bwd_args;
+
+kda_status kda_block_norm_fwd(const kda_block_norm_args *args, cudaStream_t stream);
+kda_status kda_block_norm_bwd(const kda_block_norm_bwd_args *args, cudaStream_t stream);
+size_t kda_block_norm_bwd_workspace_size(const kda_block_norm_bwd_args *args);
+
+/*
  * kda_fwd_no_alloc -- kda_fwd for callers that cannot allocate device memory.
  * (This entry point has no counterpart in the pages; it is a deployment aid.)
  *

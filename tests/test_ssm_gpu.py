@@ -1,0 +1,280 @@
+"""GPU parity of the selective scan (prompts and the decode step) against its fp64 form.
+
+Tolerances, as a share of the largest value: bf16 outputs round once at 2^-9 and their scores
+once more, so 1e-2 (the library's bound for bf16 I/O); fp32 results sum at most 128 products and
+decay, each rounding at 2^-24, so 128 * 2^-24 < 1e-5 of the summed magnitudes, doubled."""
+import numpy as np
+import pytest
+import torch
+
+import block_fp64 as ref
+
+pytestmark = pytest.mark.gpu
+TOL = {"bf16": 1e-2, "f32": 2e-5}
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def kda():
+    import gated_delta_rule_chunked_gb300 as m
+    m.library()
+    return m
+
+
+def case(lens, H, G, P, io, seed, h0=True, strength=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    T, N = sum(lens), len(lens)
+    rows = torch.nn.functional.silu(torch.randn(T, H * P + 2 * G * 128, generator=gen)).to(DT[io])
+    return dict(rows=rows, dt=torch.randn(T, H, generator=gen), a=-torch.rand(H, generator=gen) * 15 * strength - 0.1,
+                dt_bias=torch.rand(H, generator=gen) * 3 - 4.5, d_skip=torch.randn(H, generator=gen),
+                h0=torch.randn(N, H, 128, P, generator=gen) * 0.3 if h0 else None,
+                cu=torch.tensor(np.cumsum([0] + list(lens)), dtype=torch.int32))
+
+
+def split(rows, H, G, P):
+    T = rows.shape[0]
+    x, b, c = torch.split(rows, [H * P, G * 128, G * 128], 1)
+    return x.unflatten(1, (H, P)), b.unflatten(1, (G, 128)), c.unflatten(1, (G, 128))
+
+
+def cuda(t):
+    return None if t is None else t.cuda()
+
+
+def check(kda, lens, H, G, P, io, seed, h0=True, strength=1.0, views=True, **opts):
+    s = case(lens, H, G, P, io, seed, h0, strength)
+    x, b, c = split(s["rows"].cuda(), H, G, P)
+    if not views:
+        x, b, c = x.contiguous(), b.contiguous(), c.contiguous()
+    y, hT = kda.ssm_fwd(x, s["dt"].cuda(), s["a"].cuda(), b, c, s["cu"], cuda(s["h0"]), d_skip=s["d_skip"].cuda(),
+                        dt_bias=s["dt_bias"].cuda(), **opts)
+    torch.cuda.synchronize()
+    y_ref, h_ref = ref.scan(*[t for t in (x, s["dt"], s["a"], b, c)], lens, s["h0"], s["d_skip"], s["dt_bias"])
+    assert ref.rel(y.float(), y_ref) <= TOL[io]
+    assert ref.rel(hT, h_ref) <= TOL["f32"]
+    return y, hT
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,H,G,P", [
+    ([1], 1, 1, 64), ([2, 0, 7], 2, 1, 128), ([127, 128, 129], 2, 2, 64), ([8, 9, 63, 64, 65], 3, 1, 64),
+    ([300], 4, 2, 128), ([255, 1, 257], 2, 1, 128), ([700], 1, 1, 64),
+])
+def test_prompts(kda, io, lens, H, G, P):
+    check(kda, lens, H, G, P, io, seed=sum(lens) + H)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_no_initial_state_and_contiguous_inputs(kda, io):
+    check(kda, [130, 5], 2, 1, 64, io, seed=3, h0=False)
+    check(kda, [130, 5], 4, 4, 64, io, seed=4, views=False)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_strong_and_absent_decay(kda, io):
+    check(kda, [260], 3, 1, 64, io, seed=5, strength=40.0)     # most decays underflow to zero
+    s = case([200], 2, 1, 64, io, 6)
+    x, b, c = split(s["rows"].cuda(), 2, 1, 64)
+    y, hT = kda.ssm_fwd(x, s["dt"].cuda(), torch.zeros(2).cuda(), b, c, None, None)   # a = 0: prefix sums
+    y_ref, h_ref = ref.scan(x, s["dt"], torch.zeros(2), b, c, [200])
+    assert ref.rel(y.float(), y_ref) <= TOL[io] and ref.rel(hT, h_ref) <= TOL["f32"]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_raw_steps_equal_sequences_and_no_final_state(kda, io):
+    s = case([140, 140], 2, 1, 64, io, 7)
+    h = torch.rand(280, 2) * 0.2
+    h[::3] = 0.0                                               # a step of zero leaves the state as it is
+    x, b, c = split(s["rows"].cuda(), 2, 1, 64)
+    y, hT = kda.ssm_fwd(x, h.cuda(), s["a"].cuda(), b, c, None, s["h0"].cuda(), dt_softplus=False, n_seqs=2,
+                        final_state=False)
+    y_ref, _ = ref.scan(x, h, s["a"], b, c, [140, 140], s["h0"], softplus=False)
+    assert hT is None and ref.rel(y.float(), y_ref) <= TOL[io]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_sequences_are_apart(kda, io):
+    """Rows of one sequence that are not finite stay out of its neighbours."""
+    lens = [70, 131, 40, 129]
+    s = case(lens, 2, 1, 64, io, 8)
+    rows = s["rows"].cuda()
+    bad = rows.clone()
+    bad[70:201] = float("nan")
+    bad[241:] = float("inf")
+    args = (s["dt"].cuda(), s["a"].cuda())
+    run = lambda r: kda.ssm_fwd(split(r, 2, 1, 64)[0], *args, *split(r, 2, 1, 64)[1:], s["cu"].cuda(), s["h0"].cuda())
+    (y0, h0), (y1, h1) = run(rows), run(bad)
+    for lo, hi, i in ((0, 70, 0), (201, 241, 2)):
+        assert torch.equal(y0[lo:hi], y1[lo:hi]) and torch.equal(h0[i], h1[i])
+
+
+def test_chained_calls_match_one(kda):
+    """A prompt cut anywhere and continued from its state gives the same states."""
+    s = case([403], 2, 1, 64, "bf16", 9)
+    x, b, c = split(s["rows"].cuda(), 2, 1, 64)
+    dt, a = s["dt"].cuda(), s["a"].cuda()
+    y, hT = kda.ssm_fwd(x, dt, a, b, c, None, s["h0"].cuda())
+    h, ys = s["h0"].cuda(), []
+    for lo, hi in ((0, 1), (1, 130), (130, 403)):
+        yy, h = kda.ssm_fwd(x[lo:hi], dt[lo:hi], a, b[lo:hi], c[lo:hi], None, h)
+        ys.append(yy)
+    assert ref.rel(h, hT) <= TOL["f32"] and ref.rel(torch.cat(ys).float(), y.float()) <= TOL["bf16"]
+
+
+def test_same_call_same_bits(kda):
+    s = case([500, 77], 3, 1, 64, "bf16", 10)
+    x, b, c = split(s["rows"].cuda(), 3, 1, 64)
+    run = lambda: kda.ssm_fwd(x, s["dt"].cuda(), s["a"].cuda(), b, c, s["cu"].cuda(), s["h0"].cuda())
+    (y0, h0), (y1, h1) = run(), run()
+    assert torch.equal(y0, y1) and torch.equal(h0, h1)
+
+
+def test_other_stream(kda):
+    s = case([333], 2, 1, 64, "bf16", 11)
+    x, b, c = split(s["rows"].cuda(), 2, 1, 64)
+    dt, a = s["dt"].cuda(), s["a"].cuda()
+    y0, h0 = kda.ssm_fwd(x, dt, a, b, c)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y1, h1 = kda.ssm_fwd(x, dt, a, b, c)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y0, y1) and torch.equal(h0, h1)
+
+
+def test_no_tokens(kda):
+    h0 = torch.randn(2, 1, 128, 64).cuda()
+    e = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")
+    y, hT = kda.ssm_fwd(e(0, 1, 64), torch.empty(0, 1).cuda(), -torch.ones(1).cuda(), e(0, 1, 128), e(0, 1, 128),
+                        torch.zeros(3, dtype=torch.int32), h0)
+    assert y.shape == (0, 1, 64) and torch.equal(hT, h0)
+
+
+def test_refusals(kda):
+    s = case([16], 4, 2, 64, "bf16", 12)
+    x, b, c = split(s["rows"].cuda(), 4, 2, 64)
+    dt, a = s["dt"].cuda(), s["a"].cuda()
+    with pytest.raises(kda.KdaError):
+        kda.ssm_fwd(x[:, :3].contiguous(), dt[:, :3].contiguous(), a[:3], b, c)          # 2 groups, 3 heads
+    with pytest.raises(kda.KdaError):
+        kda.ssm_fwd(x.reshape(16, 8, 32), dt.repeat(1, 2), a.repeat(2), b, c)            # head_dim 32
+    with pytest.raises(ValueError):
+        kda.ssm_fwd(x.transpose(1, 2), dt, a, b, c)
+    with pytest.raises(ValueError):
+        kda.ssm_fwd(x, dt[:8], a, b, c)
+    with pytest.raises(TypeError):
+        kda.ssm_fwd(x, dt.double(), a, b, c)
+    with pytest.raises(TypeError):
+        kda.ssm_fwd(x, dt, a, b.float(), c)
+    with pytest.raises(kda.KdaError):
+        kda.ssm_fwd(x, dt, a, b, c, n_seqs=3)                                            # 16 tokens in 3 equal parts
+    with pytest.raises(kda.KdaError):                                                    # row stride 4 * 64 + 4
+        rows = torch.zeros(16, 260, dtype=torch.bfloat16, device="cuda")
+        kda.ssm_fwd(rows[:, :256].unflatten(1, (4, 64)), dt, a, b, c)
+
+
+# ------------------------------------------------------------------------------------------ step
+def step_case(N, L, H, G, P, W, io, seed, pool=None):
+    gen = torch.Generator().manual_seed(seed)
+    Cc, S = H * P + 2 * G * 128, pool or N
+    return dict(xbc=torch.randn(N, L, Cc, generator=gen).to(DT[io]), dt=torch.randn(N, L, H, generator=gen),
+                a=-torch.rand(H, generator=gen) * 8, weight=torch.randn(Cc, W, generator=gen) / W ** 0.5,
+                bias=torch.randn(Cc, generator=gen) * 0.1, conv_state=torch.randn(S, W - 1, Cc, generator=gen).to(DT[io]),
+                state=torch.randn(S, H, 128, P, generator=gen) * 0.3, d_skip=torch.randn(H, generator=gen),
+                dt_bias=torch.randn(H, generator=gen) - 2)
+
+
+def run_step(kda, s, G, act="silu", accept=None, slots=None, first=None, bias=True, skip=True):
+    g = {k: v.cuda() for k, v in s.items()}
+    N, L, _ = s["xbc"].shape
+    H, P = s["state"].shape[1], s["state"].shape[3]
+    out = torch.full((N, L, H, P), 7.0, dtype=s["xbc"].dtype, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kda.ssm_step(g["xbc"], g["dt"], g["a"], g["weight"], g["bias"] if bias else None, g["conv_state"], g["state"],
+                 cuda(accept), groups=G, d_skip=g["d_skip"] if skip else None, dt_bias=g["dt_bias"] if bias else None,
+                 activation=act, state_indices=cuda(slots), first_slot=cuda(first), out=out, dev_status=status)
+    torch.cuda.synchronize()
+    ys, pool, cpool = ref.step(s["xbc"], s["dt"], s["a"], s["weight"], s["bias"] if bias else None, s["conv_state"],
+                               s["state"], G, accept, slots, first, s["d_skip"] if skip else None,
+                               s["dt_bias"] if bias else None, act=act)
+    io = "bf16" if s["xbc"].dtype == torch.bfloat16 else "f32"
+    seen = torch.zeros(N, L, dtype=torch.bool)
+    got, want = [], []
+    for (i, t), y in ys.items():
+        seen[i, t] = True
+        got.append(out[i, t].float().cpu())
+        want.append(y)
+    if got:
+        assert ref.rel(torch.stack(got), torch.stack(want)) <= TOL[io]
+    assert (out.cpu()[~seen] == 7.0).all()                     # padding and skipped sequences are not written
+    assert ref.rel(g["state"], pool) <= TOL["f32"]
+    if cpool is not None:
+        assert torch.equal(g["conv_state"].cpu(), cpool)
+    return int(status)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("N,L,H,G,P,W", [(1, 1, 1, 1, 64, 4), (3, 4, 4, 2, 64, 4), (2, 8, 2, 1, 128, 3), (5, 2, 3, 3, 64, 2), (2, 3, 2, 1, 64, 1)])
+def test_step(kda, io, N, L, H, G, P, W):
+    s = step_case(N, L, H, G, P, W, io, seed=N * 10 + L)
+    assert run_step(kda, s, G) == 0
+    assert run_step(kda, s, G, act="none", bias=False, skip=False) == 0
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_step_accept_padding_and_pool(kda, io):
+    N, L = 9, 5
+    s = step_case(N, L, 2, 1, 64, 4, io, seed=2, pool=14)
+    slots = torch.tensor([13, 0, 4, 7, 2, 9, 1, 11, 5], dtype=torch.int32)
+    accept = torch.tensor([0, 1, 5, 2, 3, 5, 4, 9, -1], dtype=torch.int32)    # the last two are clamped
+    first = torch.tensor([0, 1, 0, 3, 2, 5, 3, 1, 0], dtype=torch.int32)      # 5: all padding
+    assert run_step(kda, s, 1, accept=accept, slots=slots, first=first) == 0
+
+
+def test_step_bad_slot(kda):
+    s = step_case(3, 2, 2, 1, 64, 4, "bf16", seed=3, pool=4)
+    assert run_step(kda, s, 1, slots=torch.tensor([1, 4, 0], dtype=torch.int32)) == 1
+    assert run_step(kda, s, 1, slots=torch.tensor([-1, -1, 9], dtype=torch.int32)) == 1
+
+
+def test_more_sequences_than_a_wave(kda):
+    s = step_case(40, 3, 24, 4, 64, 4, "bf16", seed=4)
+    accept = torch.arange(40, dtype=torch.int32) % 4
+    assert run_step(kda, s, 4, accept=accept) == 0
+
+
+def test_tokens_one_by_one_match_a_prompt(kda):
+    """The step over a prompt's raw rows reaches the states of convolution + scan in fp32."""
+    gen = torch.Generator().manual_seed(5)
+    T, H, G, P, W = 21, 2, 1, 64, 4
+    Cc = H * P + 2 * G * 128
+    s = step_case(1, T, H, G, P, W, "f32", seed=6)
+    rows = s["xbc"][0].cuda()
+    w, bias = s["weight"].cuda(), s["bias"].cuda()
+    dt, a, skip, tb = s["dt"][0].cuda(), s["a"].cuda(), s["d_skip"].cuda(), s["dt_bias"].cuda()
+    conv, tail = kda.conv_fwd(rows, w, bias, None, s["conv_state"].cuda())
+    y, hT = kda.ssm_fwd(*split(conv, H, G, P)[:1], dt, a, *split(conv, H, G, P)[1:], None, s["state"].cuda(), d_skip=skip, dt_bias=tb)
+    cs, st = s["conv_state"].cuda(), s["state"].cuda()
+    ys, t = [], 0
+    while t < T:
+        n = min(int(torch.randint(1, 9, (1,), generator=gen)), T - t)
+        ys.append(kda.ssm_step(rows[None, t:t + n].contiguous(), dt[None, t:t + n].contiguous(), a, w, bias, cs, st, groups=G,
+                               d_skip=skip, dt_bias=tb)[0])
+        t += n
+    assert ref.rel(torch.cat(ys), y) <= TOL["f32"] and ref.rel(st, hT) <= TOL["f32"] and torch.equal(cs, tail)
+
+
+def test_step_refusals(kda):
+    s = {k: v.cuda() for k, v in step_case(2, 9, 2, 1, 64, 4, "bf16", seed=7).items()}
+    call = lambda xbc, dt, **kw: kda.ssm_step(xbc, dt, s["a"], s["weight"], s["bias"], s["conv_state"], s["state"], **kw)
+    with pytest.raises(kda.KdaError):
+        call(s["xbc"], s["dt"])                                                     # 9 slots
+    x, dt = s["xbc"][:, :2].contiguous(), s["dt"][:, :2].contiguous()
+    with pytest.raises(ValueError):
+        call(x, dt, groups=2)                                                       # channels do not add up
+    with pytest.raises(ValueError):
+        call(x[:1].contiguous(), dt[:1].contiguous())                               # pool of 2, no indices
+    with pytest.raises(ValueError):
+        call(s["xbc"][:, :2], dt)                                                   # not contiguous
+    with pytest.raises(TypeError):
+        call(x, dt.half())
