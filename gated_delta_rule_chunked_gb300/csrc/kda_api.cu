@@ -84,9 +84,7 @@ WsPlan plan(const kda_fwd_args *a, bool bwd) {
 }
 
 // TMA tensor maps (the driver's cuTensorMapEncodeTiled, reached through the runtime).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using kda::EncodeTiledFn;
 
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;   // a racing second lookup stores the same pointer
@@ -218,6 +216,7 @@ int pick_slice(const kda_fwd_args *a) {
 }  // namespace
 
 void kda::set_last_error(const char *msg) { g_last_error = msg ? msg : ""; }
+kda::EncodeTiledFn kda::encode_tiled() { return encode_fn(); }
 
 extern "C" {
 

@@ -44,6 +44,8 @@ kda_status check_ssm(const kda_ssm_args *a, const char *who) {
   if (a->n_seqs < 0 || a->n_seqs > 65535 || a->total_tokens < 0 || a->total_tokens > 0x7fffffffLL)
     return fail(KDA_ERR_INVALID_ARG, who, "need 0 <= n_seqs <= 65535 and 0 <= total_tokens < 2^31");
   if (a->n_seqs == 0 && a->total_tokens > 0) return fail(KDA_ERR_INVALID_ARG, who, "tokens without sequences");
+  if ((int64_t)a->n_seqs * a->heads * (a->head_dim / kda::SSM_COLS) > 0x7fffffffLL)
+    return fail(KDA_ERR_UNSUPPORTED, who, "n_seqs * heads * head_dim / 64 must be below 2^31");
   if (!a->cu_seqlens && a->n_seqs > 0 && a->total_tokens % a->n_seqs != 0)
     return fail(KDA_ERR_INVALID_ARG, who, "without cu_seqlens total_tokens must divide into n_seqs equal sequences");
   if (!fine(a->cu_seqlens, 4) || !fine(a->dev_status, 4)) return fail(KDA_ERR_INVALID_ARG, who, "an int32 array is misaligned");
@@ -117,8 +119,9 @@ kda::BlockNormParams norm_params(const kda_block_norm_args *a) {
 extern "C" {
 
 size_t kda_ssm_fwd_workspace_size(const kda_ssm_args *a) {
-  (void)a;
-  return 0;
+  if (check_ssm(a, "kda_ssm_fwd_workspace_size") != KDA_OK || a->io_dtype == KDA_F32) return 0;
+  const int units = a->heads * (a->head_dim / kda::SSM_COLS);
+  return kda::ssm_segment_bytes(a->n_seqs, units, kda::ssm_segments(a->n_seqs, a->total_tokens, units));
 }
 
 kda_status kda_ssm_fwd(const kda_ssm_args *a, cudaStream_t stream) {
@@ -126,7 +129,12 @@ kda_status kda_ssm_fwd(const kda_ssm_args *a, cudaStream_t stream) {
   const kda_status st = check_ssm(a, who);
   if (st != KDA_OK) return st;
   if (a->n_seqs == 0) return done(cudaSuccess, who);
-  return done(kda::launch_ssm_fwd_rec(ssm_params(a), a->io_dtype == KDA_F32, stream), who);
+  if (a->io_dtype == KDA_F32) return done(kda::launch_ssm_fwd_f32(ssm_params(a), stream), who);
+  const int units = a->heads * (a->head_dim / kda::SSM_COLS), nseg = kda::ssm_segments(a->n_seqs, a->total_tokens, units);
+  const size_t need = kda::ssm_segment_bytes(a->n_seqs, units, nseg);
+  if (need > 0 && (!have(a->workspace, 16) || a->workspace_bytes < need))
+    return fail(KDA_ERR_INVALID_ARG, who, "workspace missing, misaligned or smaller than kda_ssm_fwd_workspace_size()");
+  return done(kda::launch_ssm_fwd_tc(ssm_params(a), nseg, a->workspace, stream), who);
 }
 
 size_t kda_ssm_step_workspace_size(const kda_ssm_step_args *a) {

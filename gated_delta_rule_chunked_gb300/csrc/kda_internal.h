@@ -244,7 +244,18 @@ struct SsmParams {
   float *state;
   const int *idx, *acc, *first;
 };
-cudaError_t launch_ssm_fwd_rec(const SsmParams &p, bool f32, cudaStream_t s);
+cudaError_t launch_ssm_fwd_f32(const SsmParams &p, cudaStream_t s);
+// bf16 prompts on the tensor cores. Sequences run in nseg segments; the workspace holds the first
+// nseg - 1 segments' state contributions [N][nseg - 1][units][128][64] and decays.
+struct SsmTcParams {
+  CUtensorMap tm_x, tm_b, tm_c;   // [T][row], boxes of 64 columns x 128 tokens, 128-byte swizzle
+  SsmParams s;
+  int nseg;
+  float *seg_state, *seg_decay;
+};
+int ssm_segments(int n_seqs, long long T, int units);
+size_t ssm_segment_bytes(int n_seqs, int units, int nseg);
+cudaError_t launch_ssm_fwd_tc(const SsmParams &p, int nseg, void *workspace, cudaStream_t s);
 cudaError_t launch_ssm_step(const SsmParams &p, bool f32, cudaStream_t s);
 
 // Draft verification (kda_verify.cu).
@@ -275,6 +286,12 @@ struct BlockNormParams {
 cudaError_t launch_block_norm_fwd(const BlockNormParams &p, bool f32, cudaStream_t s);
 cudaError_t launch_block_norm_bwd(const BlockNormParams &p, bool f32, cudaStream_t s);
 int block_norm_bwd_ctas(long long rows, int dim, bool f32);
+
+// cuTensorMapEncodeTiled, or null (kda_api.cu).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled();
 
 // Sets the message that kda_last_error() returns on this host thread.
 void set_last_error(const char *msg);

@@ -85,15 +85,14 @@ __device__ __forceinline__ void store_state(float *dst, int P, const float (&S)[
 }
 
 // Prompts. Grid: (value slices of all heads, sequences).
-template <typename IO>
 __global__ void __launch_bounds__(256) ssm_rec_kernel(SsmParams p) {
   __shared__ __align__(16) RecSmem sm;
   const int slices = p.P / SSM_COLS, head = blockIdx.x / slices, col0 = (blockIdx.x % slices) * SSM_COLS, n = blockIdx.y;
   const int group = head / (p.H / p.G);
   const long long t0 = p.cu ? p.cu[n] : p.T / p.n_seqs * n, t1 = p.cu ? p.cu[n + 1] : p.T / p.n_seqs * (n + 1);
-  const IO *x = static_cast<const IO *>(p.x) + (long long)head * p.P + col0;
-  const IO *b = static_cast<const IO *>(p.b) + (long long)group * SSM_N, *c = static_cast<const IO *>(p.c) + (long long)group * SSM_N;
-  IO *y = static_cast<IO *>(p.y) + (long long)head * p.P + col0;
+  const float *x = static_cast<const float *>(p.x) + (long long)head * p.P + col0;
+  const float *b = static_cast<const float *>(p.b) + (long long)group * SSM_N, *c = static_cast<const float *>(p.c) + (long long)group * SSM_N;
+  float *y = static_cast<float *>(p.y) + (long long)head * p.P + col0;
   const size_t soff = ((size_t)n * p.H + head) * SSM_N * p.P + col0;
   const float a = p.a[head], bias = p.dt_bias ? p.dt_bias[head] : 0.f, d = p.d_skip ? p.d_skip[head] : 0.f;
   float S[8][4];
@@ -101,11 +100,11 @@ __global__ void __launch_bounds__(256) ssm_rec_kernel(SsmParams p) {
   for (long long t = t0; t < t1; t += TB) {
     const int nt = (int)(t1 - t < TB ? t1 - t : TB);
     __syncthreads();   // the previous batch is consumed
-    for (int i = threadIdx.x; i < nt * SSM_COLS; i += 256) sm.x[i / SSM_COLS][i % SSM_COLS] = to_f(x[(t + i / SSM_COLS) * p.ldx + i % SSM_COLS]);
+    for (int i = threadIdx.x; i < nt * SSM_COLS; i += 256) sm.x[i / SSM_COLS][i % SSM_COLS] = (x[(t + i / SSM_COLS) * p.ldx + i % SSM_COLS]);
     for (int i = threadIdx.x; i < nt * SSM_N; i += 256) {
       const int k = i / SSM_N, e = i % SSM_N;
-      sm.b[k][e] = to_f(b[(t + k) * p.ldb + e]);
-      sm.c[k][e] = to_f(c[(t + k) * p.ldc + e]);
+      sm.b[k][e] = (b[(t + k) * p.ldb + e]);
+      sm.c[k][e] = (c[(t + k) * p.ldc + e]);
     }
     if ((int)threadIdx.x < nt) {
       const float h = step_size(p.dt[(t + threadIdx.x) * p.H + head] + bias, p.softplus);
@@ -227,10 +226,8 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmParams p, int C) {
 
 }  // namespace
 
-cudaError_t launch_ssm_fwd_rec(const SsmParams &p, bool f32, cudaStream_t s) {
-  const dim3 grid(p.H * (p.P / SSM_COLS), p.n_seqs);
-  if (f32) ssm_rec_kernel<float><<<grid, 256, 0, s>>>(p);
-  else ssm_rec_kernel<bf16><<<grid, 256, 0, s>>>(p);
+cudaError_t launch_ssm_fwd_f32(const SsmParams &p, cudaStream_t s) {
+  ssm_rec_kernel<<<dim3(p.H * (p.P / SSM_COLS), p.n_seqs), 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
