@@ -248,7 +248,7 @@ cudaError_t launch_ssm_fwd_f32(const SsmParams &p, cudaStream_t s);
 // bf16 prompts on the tensor cores. Sequences run in nseg segments; the workspace holds the first
 // nseg - 1 segments' state contributions [N][nseg - 1][units][128][64] and decays.
 struct SsmTcParams {
-  CUtensorMap tm_x, tm_b, tm_c;   // [T][row], boxes of 64 columns x 128 tokens, 128-byte swizzle
+  CUtensorMap tm_x, tm_b, tm_c, tm_y;   // [T][row], boxes of 64 columns x 128 tokens, 128-byte swizzle
   SsmParams s;
   int nseg;
   float *seg_state, *seg_decay;

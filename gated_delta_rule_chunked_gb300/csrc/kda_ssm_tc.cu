@@ -2,18 +2,21 @@
 //
 // Chunks of 128 tokens. With c_i = sum_{k <= i} h_k a log2(e) over the chunk, S the state entering it:
 //   G  = C B^T                                              [128 x 128]
-//   M  = G o 2^(c_i - c_j) h_j  (j <= i, else 0)
-//   Y  = M X + diag(2^c_i) C S + d X
+//   M  = G o 2^(c_i - c_j) h_j  (j <= i, else 0) + d I
+//   Y  = M X + diag(2^c_i) C S
 //   S' = 2^c_last S + B^T (w o X),   w_j = 2^(sum_{k > j} h_k a log2 e) h_j
 // One CTA owns 64 value columns of one (sequence, head) and walks its chunks; the state stays in the
 // registers of one warpgroup (thread = state channel), so the chain between chunks is one multiply-add
-// per element. Roles (15 warps):
-//   warps 0-3   M from G (TMEM) into TMEM as the A operand of M X; Y to memory (thread = token)
-//   warps 4-7   w o X as three bf16 terms, exact to 24 bits (thread = token)
-//   warps 8-11  the state: S' and its bf16 operand tile (thread = state channel)
-//   warp 12     the TMA loads and the chunk's scalars (softplus, the sums of h a from both ends, so
-//               that w does not come from a difference of large sums)
-//   warp 13     issues G, C S and M X;  warp 14 issues B^T (w o X)
+// per element. Roles (28 warps; a role's eight warps are two per 32 rows, each with half of the columns,
+// because the work per thread is short chains that one warp per scheduler cannot fill):
+//   warps 0-7    M from G (TMEM) into TMEM as the A operand of M X; the previous chunk's Y (thread = token)
+//   warps 8-15   w o X as three bf16 terms, exact to 24 bits (thread = token)
+//   warps 16-23  the state: S' and its bf16 operand tile (thread = state channel)
+//   warp 24      the chunk's scalars (softplus, the sums of h a from both ends, so that w does not
+//                come from a difference of large sums)
+//   warp 25      issues G, C S and M X;  warp 26 issues B^T (w o X);  warp 27 the TMA loads
+// Loops stay rolled: the roles share one instruction cache, and unrolled bodies made every chunk
+// fetch its code from beyond it (5 us a chunk instead of 2.5).
 // Rounding: the products take bf16 operands and add in fp32. X, B, C are bf16 already; M and the
 // operand copy of S are rounded once, which leaves y about as far off as its own rounding; the
 // state's update is exact to fp32, because the state is carried on and returned in fp32.
@@ -35,9 +38,10 @@ struct SsmSmem {
   static constexpr int C = 0, B = 32768, X = 65536, STAGE = 81920;   // two 64-column boxes each for C, B
   static constexpr int S = 2 * STAGE;        // state operand [128 n][64 p] bf16, MN-major
   static constexpr int WX = S + 16384;       // three terms [128 tok][64 p] bf16, MN-major
-  static constexpr int SC = WX + 3 * 16384;  // fp32 c, h, w of the chunk's tokens
-  static constexpr int BAR = SC + 3 * Q * 4;
-  static constexpr int TSLOT = BAR + 24 * 8;
+  static constexpr int SC = WX + 3 * 16384;  // fp32 c, h, w, e of the chunk's tokens
+  static constexpr int BAR = SC + 4 * Q * 4;
+  static constexpr int BARS = 40;            // places for the barriers
+  static constexpr int TSLOT = BAR + BARS * 8;
   static constexpr int BYTES = TSLOT + 16;
 };
 static_assert(SsmSmem::BYTES <= 232448, "shared memory of one SM");
@@ -46,303 +50,399 @@ static_assert(SsmSmem::BYTES <= 232448, "shared memory of one SM");
 constexpr uint32_t T_G = 0, T_M = 128, T_Y1 = 192, T_Y2 = 256, T_DS = 320;
 
 enum Bar {
-  FULL0, FULL1,      // a stage's boxes landed
-  EMPTY0, EMPTY1,    // a stage is consumed: both issuers' commits, and the 256 threads that read X rows
+  FULL0, FULL1,      // a stage's B and C landed
+  XFULL0, XFULL1,    // its X landed
+  EMPTY0, EMPTY1,    // its B and C are read: both issuers' commits
+  XEMPTY0, XEMPTY1,  // w o X has read its X
   SFULL, SEMPTY,     // the chunk's scalars written / read by all three warpgroups
   GDONE, GFREE,      // G complete / read out
-  MREADY,            // M stored
+  MREADY0, MREADY3 = MREADY0 + 3,     // M's columns 32 k .. 32 k + 31 stored (by the warps at and below the diagonal)
   YDONE, YFREE,      // both Y products complete / read out
-  WXREADY,           // w o X stored (and a short chunk's rows past its end cleared)
+  YSTAGED0, YSTAGED1,   // a stage's Y in the place of its X
+  WXREADY0, WXREADY3 = WXREADY0 + 3,  // w o X of tokens 32 k .. stored
+  DSPART0, DSPART3 = DSPART0 + 3,     // the state products have read those tokens
   DSDONE, DSFREE,    // the state products complete / read out
   SREADY,            // the state operand stored; phase 0: the initial state
+  TAIL,              // a sequence's short last chunk: the rows past its end are cleared (one phase)
   DRAIN0, DRAIN1,
   NBAR
 };
+static_assert(NBAR <= SsmSmem::BARS, "a place for every barrier");
+
+// A bounded wait in few instructions: each try may suspend the warp for about a microsecond, so the
+// tries run out after about a second.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) {
+  uint32_t ok = 0;
+  for (uint32_t k = 0; k < (1u << 19) && !ok; ++k)
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  return ok != 0;
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
-      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
+__device__ __forceinline__ void ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void st16u(uint32_t taddr, const uint32_t (&v)[16]) {
+// One box from shared memory (128-byte swizzle) to the tensor; joins the thread's bulk group.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int x, int y, const void *src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void st8u(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+// The products are issued by whole warps of which one elected lane acts: the operands then stay in
+// uniform registers, where a lone lane's would be moved there one by one for every instruction.
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
+}
+// D[tmem] (+)= A[smem] * B[smem] over one K = 16 step.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader));
+}
+// The same with A in tensor memory: A's row m is lane m, two bf16 per column.
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader));
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t *bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_u32(bar)),
+      "r"(leader)
       : "memory");
-}
-// D[tmem] (+)= A[tmem] * B[smem] over one K = 16 step: A's row m is lane m, two bf16 per column.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&v);
 }
+// The same box brought into L2 only.
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap *map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y) : "memory");
+}
+// Two fp32 lanes per instruction.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 two(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 of2(f2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(f2 a) {
+  const float2 v = of2(a);
+  return pack2(v.x, v.y);
+}
+// The two bf16 of a word as fp32.
+__device__ __forceinline__ f2 unpack2(uint32_t w) { return two(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+// Shared-memory descriptors (SWIZZLE_128B, 1024 bytes between 8-row groups) as their low word: the
+// high one is the same for all.
+__device__ __forceinline__ uint32_t dlo(uint32_t addr, uint32_t lbo) { return (addr & 0x3FFFF) >> 4 | (lbo >> 4) << 16; }
+__device__ __forceinline__ uint64_t desc(uint32_t lo) { return (uint64_t)(64u | 1u << 14 | 2u << 29) << 32 | lo; }
 // Byte offset of 16-byte chunk k of row r in a [rows][64] bf16 tile with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t row_chunk(int r, int k) { return (uint32_t)(r * 128 + ((k ^ (r & 7)) << 4)); }
 
 // STATES: the segments' own state contributions and decays only.
 template <bool STATES>
-__global__ void __launch_bounds__(480, 1) ssm_tc_kernel(const __grid_constant__ SsmTcParams p) {
+__global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ SsmTcParams p) {
   using L = SsmSmem;
   extern __shared__ __align__(1024) char smem[];
   if (smem_u32(smem) & 1023u) {   // the operand tiles' swizzle needs it; not seen
     if (threadIdx.x == 0) report(p.s.status, 3 /* KDA_ERR_CUDA */);
     return;
   }
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = tid & 127, wg = warp >> 2;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, row = tid & 127;
+  const int role = warp >> 3, half = (warp >> 2) & 1, wq = warp & 3;   // eight warps per role, two per 32 rows
   const int U = p.s.H * (p.s.P / SSM_COLS), nseg = p.nseg, runs = STATES ? nseg - 1 : nseg;
   const int u = blockIdx.x % U, ns = blockIdx.x / U, seg = ns % runs, n = ns / runs;
   const int head = u / (p.s.P / SSM_COLS), col0 = (u % (p.s.P / SSM_COLS)) * SSM_COLS, group = head / (p.s.H / p.s.G);
-  const long long seq0 = p.s.cu ? p.s.cu[n] : p.s.T / p.s.n_seqs * n, seq1 = p.s.cu ? p.s.cu[n + 1] : p.s.T / p.s.n_seqs * (n + 1);
-  const int all = (int)((seq1 - seq0 + Q - 1) / Q);
+  // token indices fit 32 bits (T < 2^31)
+  const int each = (int)(p.s.T / p.s.n_seqs), seq0 = p.s.cu ? p.s.cu[n] : each * n, seq1 = p.s.cu ? p.s.cu[n + 1] : each * (n + 1);
+  const int all = (int)(((unsigned)(seq1 - seq0) + Q - 1) / Q);
   const int first = (int)((long long)all * seg / nseg), nch = (int)((long long)all * (seg + 1) / nseg) - first;
-  const long long t_begin = seq0 + (long long)first * Q;
+  const int t_begin = seq0 + first * Q;
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + L::BAR);
   uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + L::TSLOT);
-  float *sc_c = reinterpret_cast<float *>(smem + L::SC), *sc_h = sc_c + Q, *sc_w = sc_h + Q;
+  float *sc_c = reinterpret_cast<float *>(smem + L::SC), *sc_h = sc_c + Q, *sc_w = sc_h + Q, *sc_e = sc_w + Q;
 
   if (tid == 0) {
-    const int readers = STATES ? 128 : 256;
     for (int i = 0; i < NBAR; ++i) {
-      int count = 128;
-      if (i == FULL0 || i == FULL1 || i == GDONE || i == YDONE || i == DSDONE || i == DRAIN0 || i == DRAIN1) count = 1;
-      if (i == EMPTY0 || i == EMPTY1) count = readers + (STATES ? 1 : 2);
+      int count = 256;   // every thread of a role
+      if (i == FULL0 || i == FULL1 || i == XFULL0 || i == XFULL1 || i == GDONE || i == YDONE || i == DSDONE || i == DRAIN0 || i == DRAIN1) count = 1;
+      if (i >= DSPART0 && i <= DSPART3) count = 1;
+      if (i >= MREADY0 && i <= MREADY3) count = 64 * (MREADY3 + 1 - i);
+      if (i >= WXREADY0 && i <= WXREADY3) count = 64;
       if (i == SFULL) count = 32;
-      if (i == SEMPTY) count = STATES ? 256 : 384;
+      if (i == EMPTY0 || i == EMPTY1) count = STATES ? 1 : 2;
+      if (i == SEMPTY) count = STATES ? 512 : 768;
       mbar_init(&bar[i], count);
     }
     fence_mbar_init();
   }
-  if (warp == 13) tc::alloc(tslot, 512);
+  if (warp == 25) tc::alloc(tslot, 512);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = *tslot, tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+  const uint32_t tmem = *tslot, tl = tmem + ((uint32_t)(32 * wq) << 16);
   auto len_of = [&](int c) -> int {
-    const long long left = seq1 - (t_begin + (long long)c * Q);
-    return left < Q ? (int)left : Q;
+    return min(seq1 - (t_begin + c * Q), Q);
   };
   bool ok = true;
   int c = 0;
 
-  if (wg == 0) {
+  if (role == 0) {
     if constexpr (!STATES) {
       // ------------------------------------------------------------ M and Y
       {
-        const uint32_t z[16] = {};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) st16u(tl + T_M + 16 * k, z);   // blocks above the diagonal stay zero
+        const uint32_t z[8] = {};
+#pragma unroll 1
+        for (int k = half; k < 8; k += 2) st8u(tl + T_M + 8 * k, z);   // blocks above the diagonal stay zero
         tc::wait_st();
       }
       const float d = p.s.d_skip ? p.s.d_skip[head] : 0.f;
-      bf16 *y = static_cast<bf16 *>(p.s.y) + (long long)head * p.s.P + col0;
-      const bool wide = (reinterpret_cast<uintptr_t>(p.s.y) & 31) == 0;
-      uint4 xr[8];   // the token's X row, held until its Y is there (the stage is released earlier)
-      float ei = 0.f;
-      auto store_y = [&](int k) {   // chunk k's outputs, products complete
-        const bool live = row < len_of(k);
-        bf16 *dst = y + (t_begin + (long long)k * Q + row) * (long long)p.s.H * p.s.P;
-        const uint32_t *xw = reinterpret_cast<const uint32_t *>(xr);
-        uint32_t o[32];
+      f2 e2 = two(0.f, 0.f);
+      for (c = 0; c <= nch; ++c) {
+        if (c > 0) {   // the previous chunk's Y, while this chunk's G runs
+          const int k0 = c - 1, len = len_of(k0);
+          char *ys = smem + (k0 & 1) * L::STAGE + L::X;   // in the place of the chunk's X, which everything has read by then
+          ok = wait(&bar[YDONE], k0 & 1) && wait(&bar[XEMPTY0 + (k0 & 1)], (k0 >> 1) & 1);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          tc::fence_after();
+#pragma unroll 1
+          for (int k = 2 * half; k < 2 * half + 2; ++k) {
+            float v[16], u[16];
+            uint32_t o[8];
+            tc::ld16(tl + T_Y1 + 16 * k, v);
+            tc::ld16(tl + T_Y2 + 16 * k, u);
+            tc::wait_ld();
 #pragma unroll
-        for (int hb = 0; hb < 2; ++hb) {
-          uint32_t a[32], b[32];
-          ld32(tl + T_Y1 + 32 * hb, a);
-          ld32(tl + T_Y2 + 32 * hb, b);
-          tc::wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t xx = xw[16 * hb + i];
-            const float v0 = fmaf(d, __uint_as_float(xx << 16), fmaf(ei, __uint_as_float(b[2 * i]), __uint_as_float(a[2 * i])));
-            const float v1 = fmaf(d, __uint_as_float(xx & 0xffff0000u), fmaf(ei, __uint_as_float(b[2 * i + 1]), __uint_as_float(a[2 * i + 1])));
-            o[16 * hb + i] = pack2(v0, v1);
+            for (int i = 0; i < 8; ++i) o[i] = pack2(fma2(e2, two(u[2 * i], u[2 * i + 1]), two(v[2 * i], v[2 * i + 1])));
+            *reinterpret_cast<uint4 *>(ys + row_chunk(row, 2 * k)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(ys + row_chunk(row, 2 * k + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+          tc::fence_before();
+          mbar_arrive(&bar[YFREE]);
+          fence_proxy_async();
+          mbar_arrive(&bar[YSTAGED0 + (k0 & 1)]);
+          if (len < Q && row < len) {   // a short last chunk: its box would reach into the next sequence
+            bf16 *out = static_cast<bf16 *>(p.s.y) + ((long long)(t_begin + k0 * Q + row) * p.s.H + head) * p.s.P + col0;
+#pragma unroll 1
+            for (int k = 4 * half; k < 4 * half + 4; ++k)
+              *reinterpret_cast<uint4 *>(out + 8 * k) = *reinterpret_cast<const uint4 *>(ys + row_chunk(row, k));
           }
         }
-        tc::fence_before();
-        mbar_arrive(&bar[YFREE]);
-        if (live) {
-          if (wide) {
-#pragma unroll
-            for (int k8 = 0; k8 < 4; ++k8)
-              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(dst + 16 * k8), "r"(o[8 * k8]), "r"(o[8 * k8 + 1]),
-                           "r"(o[8 * k8 + 2]), "r"(o[8 * k8 + 3]), "r"(o[8 * k8 + 4]), "r"(o[8 * k8 + 5]), "r"(o[8 * k8 + 6]), "r"(o[8 * k8 + 7])
-                           : "memory");
-          } else {
-#pragma unroll
-            for (int k4 = 0; k4 < 8; ++k4)
-              *reinterpret_cast<uint4 *>(dst + 8 * k4) = make_uint4(o[4 * k4], o[4 * k4 + 1], o[4 * k4 + 2], o[4 * k4 + 3]);
-          }
-        }
-      };
-      for (c = 0; c < nch; ++c) {
-        const char *st = smem + (c & 1) * L::STAGE;
-        ok = mbar_wait(&bar[SFULL], c & 1) && mbar_wait(&bar[GDONE], c & 1);   // G's commit covers the previous Y products
+        if (c == nch) break;
+        // M's columns are free: the products of the previous chunk were issued before this G
+        ok = wait(&bar[SFULL], c & 1) && wait(&bar[GDONE], c & 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc::fence_after();
         const float ci = sc_c[row];
-        // M: row i, 32 columns at a time, up to the warp's diagonal block
+        // M: row i, 16 columns at a time, every other block of 16 (the other half's warps take the rest). Left of the
+        // diagonal's 32 columns 2^(c_i - c_j) h_j = 2^(c_i - c_r) e_j with the last column r of j's 32,
+        // e_j = 2^(c_r - c_j) h_j (both exponents <= 0): no exponential per entry
+#pragma unroll 1
+        for (int jb = 0; jb < wq; ++jb) {
+          const int j0 = 32 * jb + 16 * half;
+          float g[16];
+          uint32_t m[8];
+          tc::ld16(tl + T_G + j0, g);
+          const float r = ex2(ci - sc_c[32 * jb + 31]);
+          const f2 r2 = two(r, r);
+          tc::wait_ld();
 #pragma unroll
-        for (int jb = 0; jb < 4; ++jb)
-          if (jb <= warp) {
-            uint32_t g[32], m[16];
-            ld32(tl + T_G + 32 * jb, g);
-            tc::wait_ld();
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 cj = *reinterpret_cast<const float4 *>(sc_c + 32 * jb + j), hj = *reinterpret_cast<const float4 *>(sc_h + 32 * jb + j);
-              float v[4] = {__uint_as_float(g[j]) * (ex2(ci - cj.x) * hj.x), __uint_as_float(g[j + 1]) * (ex2(ci - cj.y) * hj.y),
-                            __uint_as_float(g[j + 2]) * (ex2(ci - cj.z) * hj.z), __uint_as_float(g[j + 3]) * (ex2(ci - cj.w) * hj.w)};
-              if (jb == warp)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = j + e <= lane ? v[e] : 0.f;
-              m[j / 2] = pack2(v[0], v[1]);
-              m[j / 2 + 1] = pack2(v[2], v[3]);
-            }
-            st16u(tl + T_M + 16 * jb, m);
+          for (int j = 0; j < 16; j += 4) {
+            const float4 e = *reinterpret_cast<const float4 *>(sc_e + j0 + j);
+            m[j / 2] = pack2(mul2(mul2(two(g[j], g[j + 1]), two(e.x, e.y)), r2));
+            m[j / 2 + 1] = pack2(mul2(mul2(two(g[j + 2], g[j + 3]), two(e.z, e.w)), r2));
           }
-        tc::wait_st();
-        tc::fence_before();
-        mbar_arrive(&bar[GFREE]);
-        mbar_arrive(&bar[MREADY]);
-        if (c > 0) store_y(c - 1);   // its products were complete with G
-        ei = exp2f(ci);
-        ok = mbar_wait(&bar[FULL0 + (c & 1)], (c >> 1) & 1);   // complete: G read it
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          st8u(tl + T_M + j0 / 2, m);
+          tc::wait_st();
+          tc::fence_before();
+          mbar_arrive(&bar[MREADY0 + jb]);
+        }
+        {
+          const int j0 = 32 * wq + 16 * half;
+          float g[16];
+          uint32_t m[8];
+          tc::ld16(tl + T_G + j0, g);
+          tc::wait_ld();
+          tc::fence_before();
+          mbar_arrive(&bar[GFREE]);
+          const uint32_t keep = ((2u << lane) - 1u) >> (16 * half), diag = (1u << lane) >> (16 * half);   // columns j <= i, j = i
+          const f2 c2 = two(ci, ci), minus = two(-1.f, -1.f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) xr[k] = *reinterpret_cast<const uint4 *>(st + L::X + row_chunk(row, k));
-        mbar_arrive(&bar[EMPTY0 + (c & 1)]);
+          for (int j = 0; j < 16; j += 2) {
+            const float2 cj = *reinterpret_cast<const float2 *>(sc_c + j0 + j), hj = *reinterpret_cast<const float2 *>(sc_h + j0 + j);
+            const float2 x = of2(fma2(two(cj.x, cj.y), minus, c2));
+            const float2 v = of2(mul2(mul2(two(ex2(x.x), ex2(x.y)), two(hj.x, hj.y)), two(g[j], g[j + 1])));
+            m[j / 2] = pack2(add2(two(keep >> j & 1u ? v.x : 0.f, keep >> (j + 1) & 1u ? v.y : 0.f),
+                                  two(diag >> j & 1u ? d : 0.f, diag >> (j + 1) & 1u ? d : 0.f)));
+          }
+          st8u(tl + T_M + j0 / 2, m);
+          tc::wait_st();
+          tc::fence_before();
+          mbar_arrive(&bar[MREADY0 + wq]);
+        }
         mbar_arrive(&bar[SEMPTY]);
-      }
-      if (ok && nch > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bar[YDONE], (nch - 1) & 1));
-        tc::fence_after();
-        if (ok) store_y(nch - 1);
+        const float ei = exp2f(ci);
+        e2 = two(ei, ei);
       }
     }
-  } else if (wg == 1) {
+  } else if (role == 1) {
     // -------------------------------------------------------------- w o X
     for (c = 0; c < nch; ++c) {
       char *st = smem + (c & 1) * L::STAGE;
-      ok = ok && mbar_wait(&bar[SFULL], c & 1) && mbar_wait(&bar[FULL0 + (c & 1)], (c >> 1) & 1);
+      ok = ok && wait(&bar[SFULL], c & 1) && wait(&bar[XFULL0 + (c & 1)], (c >> 1) & 1);
       if (!ok) break;
-      const float w = sc_w[row];
       const bool live = row < len_of(c);
-      uint4 o[3][8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(st + L::X + row_chunk(row, k));
+      const float w = live ? sc_w[row] : 0.f;
+      if (len_of(c) < Q) {
+        ok = wait(&bar[FULL0 + (c & 1)], (c >> 1) & 1);   // the only chunk at which this role waits for B: the sequence's last
+        if (!ok) break;
+        if (!live) {   // rows past the sequence's end belong to another one, or to nobody: whatever they hold stays out
+          const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k) {
+            *reinterpret_cast<uint4 *>(st + L::B + 16384 * half + row_chunk(row, k)) = z;
+            if (k >> 2 == half) *reinterpret_cast<uint4 *>(st + L::X + row_chunk(row, k)) = z;
+          }
+        }
+        fence_proxy_async();
+        mbar_arrive(&bar[TAIL]);
+      }
+      if (c > 0) ok = wait(&bar[DSPART0 + wq], (c - 1) & 1);   // the previous terms of these tokens are read
+      if (!ok) break;
+      const f2 w2 = two(w, w), minus = two(-1.f, -1.f);
+#pragma unroll 1
+      for (int k = 4 * half; k < 4 * half + 4; ++k) {
+        const uint32_t at = row_chunk(row, k);
+        const uint4 v = *reinterpret_cast<const uint4 *>(st + L::X + at);
         const uint32_t xw[4] = {v.x, v.y, v.z, v.w};
-        uint32_t *o0 = reinterpret_cast<uint32_t *>(&o[0][k]), *o1 = reinterpret_cast<uint32_t *>(&o[1][k]), *o2 = reinterpret_cast<uint32_t *>(&o[2][k]);
+        uint32_t o0[4], o1[4], o2[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           // 24 bits in three truncated terms of 8: the remainders are exact
-          const float a = w * __uint_as_float(xw[e] << 16), b = w * __uint_as_float(xw[e] & 0xffff0000u);
-          const float a0 = __uint_as_float(__float_as_uint(a) & 0xffff0000u), b0 = __uint_as_float(__float_as_uint(b) & 0xffff0000u);
-          const float ar = a - a0, br = b - b0;
-          const float a1 = __uint_as_float(__float_as_uint(ar) & 0xffff0000u), b1 = __uint_as_float(__float_as_uint(br) & 0xffff0000u);
-          const float a2 = ar - a1, b2 = br - b1;
-          o0[e] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-          o1[e] = __byte_perm(__float_as_uint(ar), __float_as_uint(br), 0x7632);
-          o2[e] = __byte_perm(__float_as_uint(a2), __float_as_uint(b2), 0x7632);
+          const f2 v0 = mul2(w2, unpack2(xw[e]));
+          const float2 a = of2(v0);
+          const f2 v1 = fma2(two(__uint_as_float(__float_as_uint(a.x) & 0xffff0000u), __uint_as_float(__float_as_uint(a.y) & 0xffff0000u)), minus, v0);
+          const float2 b = of2(v1);
+          const float2 r = of2(fma2(two(__uint_as_float(__float_as_uint(b.x) & 0xffff0000u), __uint_as_float(__float_as_uint(b.y) & 0xffff0000u)), minus, v1));
+          o0[e] = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x7632);
+          o1[e] = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x7632);
+          o2[e] = __byte_perm(__float_as_uint(r.x), __float_as_uint(r.y), 0x7632);
         }
+        *reinterpret_cast<uint4 *>(smem + L::WX + at) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+        *reinterpret_cast<uint4 *>(smem + L::WX + 16384 + at) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+        *reinterpret_cast<uint4 *>(smem + L::WX + 32768 + at) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
       }
-      if (!live) {   // rows past the sequence's end belong to another one, or to nobody: whatever they hold stays out
-        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          o[0][k] = o[1][k] = o[2][k] = z;
-          *reinterpret_cast<uint4 *>(st + L::X + row_chunk(row, k)) = z;
-          *reinterpret_cast<uint4 *>(st + L::B + row_chunk(row, k)) = z;
-          *reinterpret_cast<uint4 *>(st + L::B + 16384 + row_chunk(row, k)) = z;
-        }
-      }
-      if (c > 0) ok = mbar_wait(&bar[DSDONE], (c - 1) & 1);   // the tile's previous terms are read
-      if (!ok) break;
-#pragma unroll
-      for (int t = 0; t < 3; ++t)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4 *>(smem + L::WX + 16384 * t + row_chunk(row, k)) = o[t][k];
       fence_proxy_async();
-      mbar_arrive(&bar[WXREADY]);
-      mbar_arrive(&bar[EMPTY0 + (c & 1)]);
+      mbar_arrive(&bar[WXREADY0 + wq]);
+      mbar_arrive(&bar[XEMPTY0 + (c & 1)]);
       mbar_arrive(&bar[SEMPTY]);
     }
-  } else if (wg == 2) {
-    // -------------------------------------------------------------- the state: row n of [128][64]
-    float S[64];
+  } else if (role == 2) {
+    // -------------------------------------------------------------- the state: row n of [128][64], 32 columns
+    f2 S[16];   // pairs of columns
     const size_t plane = (size_t)SSM_N * SSM_COLS;
-    const size_t soff = (((size_t)n * p.s.H + head) * SSM_N + row) * p.s.P + col0;
+    const size_t soff = (((size_t)n * p.s.H + head) * SSM_N + row) * p.s.P + col0 + 32 * half;
     if (!STATES && p.s.h0) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < 8; ++i) {
         const float4 v = *reinterpret_cast<const float4 *>(p.s.h0 + soff + 4 * i);
-        S[4 * i] = v.x, S[4 * i + 1] = v.y, S[4 * i + 2] = v.z, S[4 * i + 3] = v.w;
+        S[2 * i] = two(v.x, v.y), S[2 * i + 1] = two(v.z, v.w);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) S[i] = 0.f;
+      for (int i = 0; i < 16; ++i) S[i] = two(0.f, 0.f);
     }
     if (!STATES)
       for (int k = 0; k < seg; ++k) {   // the segments before this one
         const size_t at = ((size_t)n * (nseg - 1) + k) * U + u;
         const float dec = p.seg_decay[at];
-        const float *e = p.seg_state + at * plane + (size_t)row * SSM_COLS;
+        const float *e = p.seg_state + at * plane + (size_t)row * SSM_COLS + 32 * half;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
           const float4 v = __ldcg(reinterpret_cast<const float4 *>(e + 4 * i));
-          S[4 * i] = fmaf(S[4 * i], dec, v.x);
-          S[4 * i + 1] = fmaf(S[4 * i + 1], dec, v.y);
-          S[4 * i + 2] = fmaf(S[4 * i + 2], dec, v.z);
-          S[4 * i + 3] = fmaf(S[4 * i + 3], dec, v.w);
+          S[2 * i] = fma2(S[2 * i], two(dec, dec), two(v.x, v.y));
+          S[2 * i + 1] = fma2(S[2 * i + 1], two(dec, dec), two(v.z, v.w));
         }
       }
     auto put = [&]() {   // the operand tile
 #pragma unroll
-      for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4 *>(smem + L::S + row_chunk(row, k)) = tc::pack8(S + 8 * k);
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4 *>(smem + L::S + row_chunk(row, 4 * half + k)) =
+            make_uint4(pack2(S[4 * k]), pack2(S[4 * k + 1]), pack2(S[4 * k + 2]), pack2(S[4 * k + 3]));
       fence_proxy_async();
       mbar_arrive(&bar[SREADY]);
     };
     if (!STATES) put();
     float log_dec = 0.f;
     for (c = 0; c < nch; ++c) {
-      ok = mbar_wait(&bar[SFULL], c & 1);
+      ok = wait(&bar[SFULL], c & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const float last = sc_c[Q - 1];
       mbar_arrive(&bar[SEMPTY]);
       const float dec = exp2f(last);
+      const f2 dec2 = two(dec, dec);
       log_dec += last;
-      ok = mbar_wait(&bar[DSDONE], c & 1);
+      ok = wait(&bar[DSDONE], c & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::fence_after();
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float d0[16], d1[16], d2[16];
-        tc::ld16(tl + T_DS + 16 * k, d0);
-        tc::ld16(tl + T_DS + 64 + 16 * k, d1);
-        tc::ld16(tl + T_DS + 128 + 16 * k, d2);
+      for (int k = 0; k < 4; ++k) {   // 8 columns at a time: the registers hold no more
+        float d0[8], d1[8], d2[8];
+        ld8(tl + T_DS + 32 * half + 8 * k, d0);
+        ld8(tl + T_DS + 64 + 32 * half + 8 * k, d1);
+        ld8(tl + T_DS + 128 + 32 * half + 8 * k, d2);
         tc::wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) S[16 * k + i] = fmaf(S[16 * k + i], dec, d0[i] + (d1[i] + d2[i]));
+        for (int i = 0; i < 4; ++i)
+          S[4 * k + i] = fma2(S[4 * k + i], dec2, add2(two(d0[2 * i], d0[2 * i + 1]), add2(two(d1[2 * i], d1[2 * i + 1]), two(d2[2 * i], d2[2 * i + 1]))));
       }
       tc::fence_before();
       mbar_arrive(&bar[DSFREE]);
       if (!STATES && c + 1 < nch) {
-        ok = mbar_wait(&bar[YDONE], c & 1);   // C S has read the previous operand
+        ok = wait(&bar[YDONE], c & 1);   // C S has read the previous operand
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         put();
       }
@@ -351,58 +451,45 @@ __global__ void __launch_bounds__(480, 1) ssm_tc_kernel(const __grid_constant__ 
       float *dst = nullptr;
       if (STATES) {
         const size_t at = ((size_t)n * (nseg - 1) + seg) * U + u;
-        dst = p.seg_state + at * plane + (size_t)row * SSM_COLS;
-        if (row == 0) p.seg_decay[at] = exp2f(log_dec);
+        dst = p.seg_state + at * plane + (size_t)row * SSM_COLS + 32 * half;
+        if (row == 0 && half == 0) p.seg_decay[at] = exp2f(log_dec);
       } else if (p.s.hT && seg == nseg - 1) {
         dst = p.s.hT + soff;
       }
       if (dst)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) *reinterpret_cast<float4 *>(dst + 4 * i) = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+        for (int i = 0; i < 8; ++i) {
+          const float2 a = of2(S[2 * i]), b = of2(S[2 * i + 1]);
+          *reinterpret_cast<float4 *>(dst + 4 * i) = make_float4(a.x, a.y, b.x, b.y);
+        }
     }
-  } else if (warp == 12) {
-    // -------------------------------------------------------------- loads and scalars
-    auto issue = [&](int k) {   // lane 0
-      char *st = smem + (k & 1) * L::STAGE;
-      uint64_t *b = &bar[FULL0 + (k & 1)];
-      const int t = (int)(t_begin + (long long)k * Q);
-      mbar_expect_tx(b, STATES ? 49152 : 81920);
-      if (!STATES) {
-        tc::tma_load_2d(st + L::C, &p.tm_c, group * SSM_N, t, b);
-        tc::tma_load_2d(st + L::C + 16384, &p.tm_c, group * SSM_N + 64, t, b);
-      }
-      tc::tma_load_2d(st + L::B, &p.tm_b, group * SSM_N, t, b);
-      tc::tma_load_2d(st + L::B + 16384, &p.tm_b, group * SSM_N + 64, t, b);
-      tc::tma_load_2d(st + L::X, &p.tm_x, head * p.s.P + col0, t, b);
-    };
+  } else if (warp == 24) {
+    // -------------------------------------------------------------- scalars: lane l has tokens 4 l .. 4 l + 3
     const float al = p.s.a[head] * LOG2E, bias = p.s.dt_bias ? p.s.dt_bias[head] : 0.f;
     auto fetch = [&](int k, float (&v)[4]) {
       const int len = len_of(k);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = 4 * lane + i;
-        v[i] = t < len ? p.s.dt[(t_begin + (long long)k * Q + t) * p.s.H + head] : 0.f;
+        v[i] = t < len ? p.s.dt[(long long)(t_begin + k * Q + t) * p.s.H + head] : 0.f;
       }
     };
-    int issued = 0;
     float v[4];
     if (nch > 0) fetch(0, v);
-    if (lane == 0)
-      while (issued < nch && issued < 2) issue(issued++);
-    issued = nch < 2 ? nch : 2;
     for (c = 0; c < nch; ++c) {
-      if (c > 0) ok = mbar_wait(&bar[SEMPTY], (c - 1) & 1);
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const int len = len_of(c);
-      float h[4], la[4], pre[4], suf[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float b = v[i] + bias;
-        h[i] = p.s.softplus ? log1pf(expf(-fabsf(b))) + fmaxf(b, 0.f) : b;
-        if (4 * lane + i >= len) h[i] = 0.f;
-        la[i] = h[i] * al;
-      }
+      float h[4] = {v[0], v[1], v[2], v[3]};
       if (c + 1 < nch) fetch(c + 1, v);
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {   // one body for the four: the values rotate
+        const float b = h[0] + bias;
+        const float x = p.s.softplus ? log1pf(expf(-fabsf(b))) + fmaxf(b, 0.f) : b;
+        h[0] = h[1], h[1] = h[2], h[2] = h[3];
+        h[3] = 4 * lane + i < len ? x : 0.f;
+      }
+      float la[4], pre[4], suf[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) la[i] = h[i] * al;
       pre[0] = la[0];
 #pragma unroll
       for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + la[i];
@@ -418,95 +505,144 @@ __global__ void __launch_bounds__(480, 1) ssm_tc_kernel(const __grid_constant__ 
       }
       const float left = __shfl_up_sync(0xffffffffu, below, 1), right = __shfl_down_sync(0xffffffffu, above, 1);
       const float bl = lane > 0 ? left : 0.f, ab = lane < 31 ? right : 0.f;
-      *reinterpret_cast<float4 *>(sc_c + 4 * lane) = make_float4(bl + pre[0], bl + pre[1], bl + pre[2], bl + pre[3]);
+      const float end = __shfl_sync(0xffffffffu, below, lane | 7);   // c at the last token of the lane's block of 32
+      float e[4], w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        pre[i] += bl;
+        e[i] = h[i] * ex2(end - pre[i]);
+        w[i] = h[i] * exp2f(suf[i] + ab);
+      }
+      // everything above ran beside the previous chunk; only the stores wait for its readers
+      if (c > 0) ok = wait(&bar[SEMPTY], (c - 1) & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      *reinterpret_cast<float4 *>(sc_c + 4 * lane) = make_float4(pre[0], pre[1], pre[2], pre[3]);
       *reinterpret_cast<float4 *>(sc_h + 4 * lane) = make_float4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<float4 *>(sc_w + 4 * lane) =
-          make_float4(h[0] * exp2f(suf[0] + ab), h[1] * exp2f(suf[1] + ab), h[2] * exp2f(suf[2] + ab), h[3] * exp2f(suf[3] + ab));
+      *reinterpret_cast<float4 *>(sc_e + 4 * lane) = make_float4(e[0], e[1], e[2], e[3]);
+      *reinterpret_cast<float4 *>(sc_w + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
       mbar_arrive(&bar[SFULL]);
-      if (c > 0 && c + 1 < nch) {   // the previous chunk's stage is the next chunk's
-        if (lane == 0) {
-          ok = mbar_wait(&bar[EMPTY0 + ((c + 1) & 1)], ((c - 1) >> 1) & 1);
-          if (ok) issue(c + 1);
-        }
-        if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
-        issued = c + 2;
-      }
     }
-    // every copy has landed before the CTA leaves, also after a timeout
-    if (lane == 0)
-      for (int k = issued > 2 ? issued - 2 : 0; k < issued; ++k) mbar_wait(&bar[FULL0 + (k & 1)], (k >> 1) & 1);
-    __syncwarp();
-  } else if (warp == 13) {
+  } else if (warp == 27) {
+    // -------------------------------------------------------------- loads
     if (lane == 0) {
-      if constexpr (!STATES) {
-        // ---------------------------------------------------------- G, C S, M X
-        const uint64_t d_s = tc::desc_sw128_mn(smem_u32(smem + L::S), 8192);
-        for (c = 0; c < nch; ++c) {
-          const uint32_t st = smem_u32(smem + (c & 1) * L::STAGE);
-          ok = mbar_wait(&bar[FULL0 + (c & 1)], (c >> 1) & 1);
-          if (ok && c > 0) ok = mbar_wait(&bar[GFREE], (c - 1) & 1);
-          if (ok && len_of(c) < Q) {   // rows past the end must be cleared; the barrier's previous phase first, so that parities tell
-            if (c > 0) ok = mbar_wait(&bar[WXREADY], (c - 1) & 1);
-            ok = ok && mbar_wait(&bar[WXREADY], c & 1);
-          }
-          if (!ok) break;
-          tc::fence_after();
-          const uint64_t d_c = tc::desc_sw128(st + L::C), d_b = tc::desc_sw128(st + L::B), d_x = tc::desc_sw128_mn(st + L::X, 8192);
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const uint32_t o = (ks >> 2) * (16384 >> 4) + (ks & 3) * 2;
-            tc::mma_bf16(tmem + T_G, d_c + o, d_b + o, tc::idesc_bf16(128, 128), ks > 0);
-          }
-          tc::commit(&bar[GDONE]);
-          ok = mbar_wait(&bar[SREADY], c & 1);
-          if (ok && c > 0) ok = mbar_wait(&bar[YFREE], (c - 1) & 1);
-          if (!ok) break;
-          tc::fence_after();
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const uint32_t o = (ks >> 2) * (16384 >> 4) + (ks & 3) * 2;
-            tc::mma_bf16(tmem + T_Y2, d_c + o, d_s + ks * (2048 >> 4), tc::idesc_bf16_mn(128, 64, false, true), ks > 0);
-          }
-          ok = mbar_wait(&bar[MREADY], c & 1);
-          if (!ok) break;
-          tc::fence_after();
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_ts(tmem + T_Y1, tmem + T_M + 8 * ks, d_x + ks * (2048 >> 4), tc::idesc_bf16_mn(128, 64, false, true), ks > 0);
-          tc::commit(&bar[YDONE]);
-          tc::commit(&bar[EMPTY0 + (c & 1)]);
+      int issued = 0, xissued = 0;
+      // chunk k's outputs leave as one box from the place of its X tile
+      auto store = [&](int k) {
+        if (!wait(&bar[YSTAGED0 + (k & 1)], (k >> 1) & 1)) return false;
+        if (len_of(k) == Q) {
+          tma_store_2d(&p.tm_y, head * p.s.P + col0, t_begin + k * Q, smem + (k & 1) * L::STAGE + L::X);
+          bulk_commit();
+          bulk_wait_read();
         }
-        tc::commit(&bar[DRAIN0]);   // nothing of this thread runs on once the CTA leaves
-        ok &= mbar_wait(&bar[DRAIN0], 0);
-      }
-    }
-    __syncwarp();
-  } else {
-    if (lane == 0) {
-      // ------------------------------------------------------------ B^T (w o X)
-      const uint64_t d_w = tc::desc_sw128_mn(smem_u32(smem + L::WX), 16384);
-      for (c = 0; c < nch; ++c) {
-        ok = mbar_wait(&bar[WXREADY], c & 1);
-        if (ok && c > 0) ok = mbar_wait(&bar[DSFREE], (c - 1) & 1);
+        return true;
+      };
+#pragma unroll 1
+      for (c = 0; c < nch + (STATES ? 0 : 2); ++c) {
+        char *st = smem + (c & 1) * L::STAGE;
+        const int t = t_begin + c * Q;
+        if (c < nch) {   // B and C first: they are free before Y has left from X's place
+          if (c >= 2) ok = wait(&bar[EMPTY0 + (c & 1)], ((c >> 1) - 1) & 1);
+          if (!ok) break;
+          uint64_t *b = &bar[FULL0 + (c & 1)];
+          mbar_expect_tx(b, STATES ? 32768 : 65536);
+          for (int k = 0; k < (STATES ? 2 : 4); ++k)   // B's two halves, C's two
+            tc::tma_load_2d(st + (k < 2 ? L::B : L::C) + 16384 * (k & 1), k < 2 ? &p.tm_b : &p.tm_c, group * SSM_N + 64 * (k & 1), t, b);
+          issued = c + 1;
+          if (c + 1 < nch) {   // the next chunk's boxes into L2
+            for (int k = 0; k < (STATES ? 2 : 4); ++k) prefetch_2d(k < 2 ? &p.tm_b : &p.tm_c, group * SSM_N + 64 * (k & 1), t + Q);
+            prefetch_2d(&p.tm_x, head * p.s.P + col0, t + Q);
+          }
+        }
+        if (c >= 2) ok = STATES ? wait(&bar[XEMPTY0 + (c & 1)], ((c >> 1) - 1) & 1) : store(c - 2);
         if (!ok) break;
-        tc::fence_after();
-        const uint64_t d_b = tc::desc_sw128_mn(smem_u32(smem + (c & 1) * L::STAGE + L::B), 16384);
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc::mma_bf16(tmem + T_DS, d_b + ks * (2048 >> 4), d_w + ks * (2048 >> 4), tc::idesc_bf16_mn(128, 192, true, true), ks > 0);
-        tc::commit(&bar[DSDONE]);
-        tc::commit(&bar[EMPTY0 + (c & 1)]);
+        if (c < nch) {
+          mbar_expect_tx(&bar[XFULL0 + (c & 1)], 16384);
+          tc::tma_load_2d(st + L::X, &p.tm_x, head * p.s.P + col0, t, &bar[XFULL0 + (c & 1)]);
+          xissued = c + 1;
+        }
       }
-      tc::commit(&bar[DRAIN1]);
-      ok &= mbar_wait(&bar[DRAIN1], 0);
+      // every copy has landed, in either direction, before the CTA leaves, also after a timeout
+#pragma unroll 1
+      for (int k = issued > 2 ? issued - 2 : 0; k < issued; ++k) wait(&bar[FULL0 + (k & 1)], (k >> 1) & 1);
+#pragma unroll 1
+      for (int k = xissued > 2 ? xissued - 2 : 0; k < xissued; ++k) wait(&bar[XFULL0 + (k & 1)], (k >> 1) & 1);
+      if (!STATES) bulk_wait_all();
     }
     __syncwarp();
+  } else if (warp == 25) {
+    if constexpr (!STATES) {
+      // ------------------------------------------------------------ G, C S, M X
+      const uint32_t leader = elect();
+      const uint32_t d_s = dlo(smem_u32(smem + L::S), 8192);
+      auto all = [&](bool w) { return (bool)__all_sync(0xffffffffu, w); };
+#pragma unroll 1
+      for (c = 0; c < nch; ++c) {
+        const uint32_t st = smem_u32(smem + (c & 1) * L::STAGE);
+        const uint32_t d_c = dlo(st + L::C, 16), d_b = dlo(st + L::B, 16), d_x = dlo(st + L::X, 8192);
+        ok = wait(&bar[FULL0 + (c & 1)], (c >> 1) & 1) && (c == 0 || wait(&bar[GFREE], (c - 1) & 1)) && (len_of(c) == Q || wait(&bar[TAIL], 0));
+        if (!(ok = all(ok))) break;
+        tc::fence_after();
+#pragma unroll
+        for (uint32_t ks = 0; ks < 8; ++ks) {
+          const uint32_t o = (ks >> 2) * (16384 >> 4) + (ks & 3) * 2;
+          mma_ss(leader, tmem + T_G, desc(d_c + o), desc(d_b + o), tc::idesc_bf16(128, 128), ks > 0);
+        }
+        commit(leader, &bar[GDONE]);
+        ok = wait(&bar[SREADY], c & 1) && (c == 0 || wait(&bar[YFREE], (c - 1) & 1));
+        if (!(ok = all(ok))) break;
+        tc::fence_after();
+#pragma unroll
+        for (uint32_t ks = 0; ks < 8; ++ks)
+          mma_ss(leader, tmem + T_Y2, desc(d_c + (ks >> 2) * (16384 >> 4) + (ks & 3) * 2), desc(d_s + ks * (2048 >> 4)),
+                 tc::idesc_bf16_mn(128, 64, false, true), ks > 0);
+        commit(leader, &bar[EMPTY0 + (c & 1)]);
+        ok = wait(&bar[XFULL0 + (c & 1)], (c >> 1) & 1);
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) {   // as M's column blocks become ready
+          ok = ok && all(wait(&bar[MREADY0 + k], c & 1));
+          if (ok) {
+            tc::fence_after();
+            mma_ts(leader, tmem + T_Y1, tmem + T_M + 16 * k, desc(d_x + k * (4096 >> 4)), tc::idesc_bf16_mn(128, 64, false, true), k > 0);
+            mma_ts(leader, tmem + T_Y1, tmem + T_M + 16 * k + 8, desc(d_x + k * (4096 >> 4) + (2048 >> 4)), tc::idesc_bf16_mn(128, 64, false, true), 1);
+          }
+        }
+        if (!ok) break;
+        commit(leader, &bar[YDONE]);
+      }
+      commit(leader, &bar[DRAIN0]);   // nothing of this thread runs on once the CTA leaves
+      ok &= wait(&bar[DRAIN0], 0);
+    }
+  } else {
+    // -------------------------------------------------------------- B^T (w o X)
+    const uint32_t leader = elect();
+    const uint32_t d_w = dlo(smem_u32(smem + L::WX), 16384);
+#pragma unroll 1
+    for (c = 0; c < nch; ++c) {
+      const uint32_t d_b = dlo(smem_u32(smem + (c & 1) * L::STAGE + L::B), 16384);
+      ok = wait(&bar[FULL0 + (c & 1)], (c >> 1) & 1) && (c == 0 || wait(&bar[DSFREE], (c - 1) & 1));
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k) {
+        ok = __all_sync(0xffffffffu, ok && wait(&bar[WXREADY0 + k], c & 1));
+        if (ok) {
+          tc::fence_after();
+          mma_ss(leader, tmem + T_DS, desc(d_b + k * (4096 >> 4)), desc(d_w + k * (4096 >> 4)), tc::idesc_bf16_mn(128, 192, true, true), k > 0);
+          mma_ss(leader, tmem + T_DS, desc(d_b + k * (4096 >> 4) + (2048 >> 4)), desc(d_w + k * (4096 >> 4) + (2048 >> 4)),
+                 tc::idesc_bf16_mn(128, 192, true, true), 1);
+          commit(leader, &bar[DSPART0 + k]);
+        }
+      }
+      if (!ok) break;
+      commit(leader, &bar[DSDONE]);
+      commit(leader, &bar[EMPTY0 + (c & 1)]);
+    }
+    commit(leader, &bar[DRAIN1]);
+    ok &= wait(&bar[DRAIN1], 0);
   }
   if (!ok) report(p.s.status, ERR_TIMEOUT);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (warp == 13) tc::dealloc(tmem, 512);
+  if (warp == 25) tc::dealloc(tmem, 512);
 }
 
 bool map_rows(EncodeTiledFn fn, CUtensorMap *m, const void *base, long long rows, long long width, long long ld) {
@@ -518,9 +654,11 @@ bool map_rows(EncodeTiledFn fn, CUtensorMap *m, const void *base, long long rows
 }
 }  // namespace
 
-// Segments per sequence: the count that takes the fewest chunk times. Without segments every wave of
-// CTAs walks whole sequences; with k, a wave walks 1/k of them, at 1.45 times the work (the state
-// products run twice) and some fixed cost for the second launch and the folding.
+// Segments per sequence: the count that takes the fewest chunk times (about 2 us each). Without segments
+// every wave of CTAs walks whole sequences; with k, a wave walks 1/k of them, in two passes of which the
+// first costs about as much as the second (at 96 heads of one 32768-token prompt, 0.52 ms without and
+// 0.76 ms with 11 segments; at 24 units of 4096 tokens, 0.11 and 0.07 ms), plus the second launch and the
+// folding.
 int ssm_segments(int n_seqs, long long T, int units) {
   if (n_seqs < 1 || T < 1) return 1;
   int dev = 0, sms = 0;
@@ -532,7 +670,7 @@ int ssm_segments(int n_seqs, long long T, int units) {
   int best = 1;
   double cost = chunks * (double)(long long)((pairs + sms - 1) / sms);
   for (int k = 2; k <= 16 && k * 2 <= chunks; ++k) {
-    const double t = 1.45 * chunks / k * (double)(long long)((pairs * k + sms - 1) / sms) + 6.0 + 0.5 * k;
+    const double t = 2.0 * chunks / k * (double)(long long)((pairs * k + sms - 1) / sms) + 4.0 + 0.5 * k;
     if (t < cost) cost = t, best = k;
   }
   return best;
@@ -553,7 +691,8 @@ cudaError_t launch_ssm_fwd_tc(const SsmParams &s, int nseg, void *workspace, cud
   if (!fn) return cudaErrorNotSupported;
   const long long rows = s.T > 0 ? s.T : 1;
   if (s.T > 0 && (!map_rows(fn, &p.tm_x, s.x, rows, (long long)s.H * s.P, s.ldx) || !map_rows(fn, &p.tm_b, s.b, rows, (long long)s.G * SSM_N, s.ldb) ||
-                  !map_rows(fn, &p.tm_c, s.c, rows, (long long)s.G * SSM_N, s.ldc)))
+                  !map_rows(fn, &p.tm_c, s.c, rows, (long long)s.G * SSM_N, s.ldc) ||
+                  !map_rows(fn, &p.tm_y, s.y, rows, (long long)s.H * s.P, (long long)s.H * s.P)))
     return cudaErrorInvalidValue;
   if ((size_t)s.n_seqs * nseg * U > 0x7fffffffu) return cudaErrorInvalidConfiguration;
   const size_t items = nseg > 1 ? (size_t)s.n_seqs * (nseg - 1) * U : 0;
@@ -564,11 +703,11 @@ cudaError_t launch_ssm_fwd_tc(const SsmParams &s, int nseg, void *workspace, cud
   if (nseg > 1) {
     e = cudaFuncSetAttribute(ssm_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SsmSmem::BYTES);
     if (e != cudaSuccess) return e;
-    ssm_tc_kernel<true><<<(unsigned)items, 480, SsmSmem::BYTES, st>>>(p);
+    ssm_tc_kernel<true><<<(unsigned)items, 896, SsmSmem::BYTES, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  ssm_tc_kernel<false><<<(unsigned)((size_t)s.n_seqs * nseg * U), 480, SsmSmem::BYTES, st>>>(p);
+  ssm_tc_kernel<false><<<(unsigned)((size_t)s.n_seqs * nseg * U), 896, SsmSmem::BYTES, st>>>(p);
   return cudaGetLastError();
 }
 
