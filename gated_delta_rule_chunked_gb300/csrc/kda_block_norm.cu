@@ -7,6 +7,7 @@
 //   dx = D + r_x (E w_pre) - x r_x^3 mean((E w_pre) x),  dresidual = dx,  dw_pre = sum E x r_x
 //   A = sum dx h per column, so dscale = w_post A and dw_post = scale A (one accumulator)
 //   t = dx scale w_post,  dz = t hat act'(z),  dhat = t act(z),  du = r_u (dhat - hat mean(dhat hat))
+// (dhat hat = dx m summed over a row, with m = scale w_post h)
 // Memory-bound: every tensor is read and written once, everything in between is fp32 registers.
 // A row is owned by LPR lanes of a warp (short rows) or by a whole CTA (LPR = 0), each thread
 // holding VPT vectors of 8 elements.
@@ -21,6 +22,7 @@ template <typename IO> struct Raw;
 template <> struct Raw<bf16> {
   uint4 v;
   __device__ __forceinline__ void load(const bf16 *p) { v = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void loads(const char *p) { v = *reinterpret_cast<const uint4 *>(p); }   // from shared memory
   __device__ __forceinline__ void get(float (&x)[8]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -35,6 +37,10 @@ template <> struct Raw<float> {
   __device__ __forceinline__ void load(const float *p) {
     a = __ldcs(reinterpret_cast<const float4 *>(p));
     b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+  }
+  __device__ __forceinline__ void loads(const char *p) {
+    a = *reinterpret_cast<const float4 *>(p);
+    b = *(reinterpret_cast<const float4 *>(p) + 1);
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
@@ -67,33 +73,145 @@ __device__ __forceinline__ void col8(const float *w, int c, float (&x)[8]) {
   }
 }
 
-// Sum over the lanes that share a row. CTA rows: `red` holds two sets of per-warp partials that
-// consecutive calls alternate (`set`), so one barrier per call is enough: a set is rewritten only
-// after the barrier of the call in between.
+// Sum over the LPR lanes that share a row.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// Sum over a row that is the CTA's. `red` holds two sets of per-warp partials that consecutive calls
+// alternate (`set`), so one barrier per call is enough.
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v, float *red, int set) {
-  constexpr int W = LPR ? LPR : 32;
-#pragma unroll
-  for (int o = W / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if constexpr (LPR == 0) {
+  if constexpr (LPR != 0) {
+    return row_sum<LPR>(v);
+  } else {
+    v = row_sum<32>(v);
     const int nw = blockDim.x >> 5;
     float *r = red + set * 32;
     if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
     __syncthreads();
     v = 0.f;
     for (int w = 0; w < nw; ++w) v += r[w];
+    return v;
   }
-  return v;
 }
 
-template <bool SILU>
-__device__ __forceinline__ float gate_of(float z) {
-  const float s = __fdividef(1.f, 1.f + __expf(-z));
-  return SILU ? z * s : s;
+// 1 / (1 + e^-z), by the hardware's 2^x and reciprocal (a few units of 2^-23 each).
+__device__ __forceinline__ float sigmoid(float z) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(z * -LOG2E));
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(1.f + e));
+  return r;
 }
+enum { GATE_NONE = 0, GATE_SIGMOID = 1, GATE_SILU = 2 };
+template <int GATE>
+__device__ __forceinline__ float gate_of(float z) {
+  return GATE == GATE_SILU ? z * sigmoid(z) : sigmoid(z);
+}
+
+// The backward of 8 columns of a row. Both sums of a row's gradient come from one pass, because
+// dx = dx0 - x cx with dx0 = D + r_x E w_pre known before the sums and cx = r_x^3 mean(E w_pre x) after:
+//   sum dhat hat = sum dx m = sum dx0 m - cx sum x m
+// so a row has one reduction, of three values. The column vectors and the sums over rows stay in registers.
+template <typename IO>
+struct BwdCols {
+  float ws[8], wp[8], A[8], P[8];   // w_post scale, w_pre, the sums over rows
+  __device__ __forceinline__ BwdCols(const BlockNormParams &p, int c) {
+    float sc[8];
+    col8(p.w_post, c, ws);
+    col8(p.scale, c, sc);
+    col8(p.w_pre, c, wp);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      ws[e] *= sc[e];
+      A[e] = P[e] = 0.f;
+    }
+  }
+};
+template <typename IO, int GATE>
+struct BwdRow {   // what the second half of a row needs of the first, beside u and z
+  float x[8], dx[8], ru, rx;
+  // s = {sum (E w_pre) x, sum dx0 m, sum x m} of these columns.
+  __device__ __forceinline__ void first(const BlockNormParams &p, BwdCols<IO> &col, const Raw<IO> &u, const Raw<IO> &z, const Raw<IO> &res, const Raw<IO> &dn,
+                                        const Raw<IO> &dout, float (&s)[3]) {
+    float m[8], t[8];
+    u.get(m);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m[e] *= ru * col.ws[e];
+    if (GATE) {
+      z.get(t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m[e] *= gate_of<GATE>(t[e]);
+    }
+    if (p.residual) {
+      res.get(x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] += m[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = m[e];
+    }
+    if (p.d_out) {
+      dout.get(dx);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dx[e] = 0.f;
+    }
+    if (p.d_normed) {
+      dn.get(t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float n = t[e] * rx, f = n * col.wp[e];
+        col.P[e] = fmaf(n, x[e], col.P[e]);
+        s[0] = fmaf(f, x[e], s[0]);   // r_x times the sum; made up for below
+        dx[e] += f;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      s[1] = fmaf(dx[e], m[e], s[1]);
+      s[2] = fmaf(x[e], m[e], s[2]);
+    }
+  }
+  // With the row's sums: the gradients of its columns, and A.
+  __device__ __forceinline__ void second(const BlockNormParams &p, BwdCols<IO> &col, const Raw<IO> &u, const Raw<IO> &z, const float (&s)[3],
+                                         long long base) {
+    const float cx = s[0] * p.inv_dim * rx * rx, ch = p.w_post ? (s[1] - cx * s[2]) * p.inv_dim : 0.f;
+    float hat[8], t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dx[e] = fmaf(-cx, x[e], dx[e]);
+    if (p.residual) store8(static_cast<IO *>(p.d_residual) + base, dx);
+    u.get(hat);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) hat[e] *= ru;
+    if (GATE) {
+      z.get(t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float sg = sigmoid(t[e]), g = GATE == GATE_SILU ? t[e] * sg : sg, v = dx[e] * hat[e];
+        // act' = sg + g (1 - sg) for SiLU, sg (1 - sg) for the sigmoid
+        t[e] = v * col.ws[e] * (GATE == GATE_SILU ? fmaf(-g, sg, sg + g) : fmaf(-sg, sg, sg));
+        col.A[e] = fmaf(v, g, col.A[e]);
+        dx[e] *= col.ws[e] * g;
+      }
+      store8(static_cast<IO *>(p.d_gate) + base, t);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        col.A[e] = fmaf(dx[e], hat[e], col.A[e]);
+        dx[e] *= col.ws[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dx[e] = ru * fmaf(-ch, hat[e], dx[e]);
+    store8(static_cast<IO *>(p.du) + base, dx);
+  }
+};
 
 // One row per (CTA or LPR lanes); the grid covers all rows.
-template <typename IO, int LPR, int VPT>
+template <typename IO, int GATE, int LPR, int VPT>
 __global__ void __launch_bounds__(LPR ? 256 : 512) block_norm_fwd_kernel(BlockNormParams p) {
   __shared__ float red[64];
   const int lane = LPR ? (threadIdx.x & (LPR - 1)) : threadIdx.x, step = LPR ? LPR : blockDim.x;
@@ -107,7 +225,7 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) block_norm_fwd_kernel(BlockNo
     const int v = lane + step * j;
     if (live && v < nvec) {
       u[j].load(static_cast<const IO *>(p.u) + base + v * 8);
-      if (p.gate) z[j].load(static_cast<const IO *>(p.gate) + base + v * 8);
+      if (GATE) z[j].load(static_cast<const IO *>(p.gate) + base + v * 8);
       if (p.residual) r[j].load(static_cast<const IO *>(p.residual) + base + v * 8);
     }
   }
@@ -135,10 +253,10 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) block_norm_fwd_kernel(BlockNo
       col8(p.w_post, v * 8, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[j][e] *= ru * w[e];
-      if (p.gate) {
+      if (GATE) {
         z[j].get(g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[j][e] *= p.silu ? gate_of<true>(g[e]) : gate_of<false>(g[e]);
+        for (int e = 0; e < 8; ++e) x[j][e] *= gate_of<GATE>(g[e]);
       }
       if (p.scale) {
         col8(p.scale, v * 8, w);
@@ -171,176 +289,196 @@ __global__ void __launch_bounds__(LPR ? 256 : 512) block_norm_fwd_kernel(BlockNo
   }
 }
 
-// Persistent: CTA b takes row groups b, b + gridDim, ...; a thread keeps its columns, so A and
-// dw_pre accumulate in registers. partial[b][2][d] at the end (the CTA's row groups added in a
-// fixed order), summed over b by block_norm_dw_kernel.
-template <typename IO, int LPR, int VPT>
-__global__ void __launch_bounds__(LPR ? 256 : 512) block_norm_bwd_kernel(BlockNormParams p) {
-  extern __shared__ float bn_smem[];   // LPR rows: [2][rows per CTA][d] partials
-  __shared__ float red[64];
-  constexpr int L1 = LPR ? LPR : 1;
-  const int lane = LPR ? (threadIdx.x & (L1 - 1)) : threadIdx.x, step = LPR ? LPR : blockDim.x;
-  const int rpc = LPR ? blockDim.x / L1 : 1, sub = LPR ? threadIdx.x / L1 : 0;
-  const int nvec = p.dim >> 3;
-  float A[VPT][8], P[VPT][8];
-#pragma unroll
-  for (int j = 0; j < VPT; ++j)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) A[j][e] = P[j][e] = 0.f;
+// Short rows. Persistent: CTA b takes row groups b, b + gridDim, ...; a thread keeps its 8 columns, so A
+// and dw_pre accumulate in registers. partial[b][2][d] at the end (the CTA's rows added in a fixed
+// order), summed over b by block_norm_dw_kernel.
+template <typename IO, int GATE, int LPR>
+__global__ void __launch_bounds__(256) block_norm_bwd_short_kernel(BlockNormParams p) {
+  extern __shared__ float bn_smem[];   // [2][rows per CTA][d] partials
+  const int lane = threadIdx.x & (LPR - 1), rpc = blockDim.x / LPR, sub = threadIdx.x / LPR;
+  const int c = lane * 8;
+  const bool in = c < p.dim;
+  BwdCols<IO> col(p, in ? c : 0);
   for (long long row0 = (long long)blockIdx.x * rpc; row0 < p.rows; row0 += (long long)gridDim.x * rpc) {
-    const long long row = row0 + sub, base = row * p.dim;
-    const bool live = row < p.rows;
-    const float ru = live && p.w_post ? p.rstd_post[row] : 1.f, rx = live && p.w_pre ? p.rstd_pre[row] : 0.f;
-    float x[VPT][8], ep[VPT][8], s = 0.f;   // out, E w_pre
-    Raw<IO> u[VPT], z[VPT];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = lane + step * j;
-      if (live && v < nvec) {
-        u[j].load(static_cast<const IO *>(p.u) + base + v * 8);
-        if (p.gate) z[j].load(static_cast<const IO *>(p.gate) + base + v * 8);
-        if (p.w_pre) {
-          Raw<IO> r, en;
-          float w[8], t[8];
-          if (p.residual) r.load(static_cast<const IO *>(p.residual) + base + v * 8);
-          if (p.d_normed) en.load(static_cast<const IO *>(p.d_normed) + base + v * 8);
-          u[j].get(x[j]);
-          col8(p.w_post, v * 8, w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[j][e] *= ru * w[e];
-          if (p.gate) {
-            z[j].get(t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[j][e] *= p.silu ? gate_of<true>(t[e]) : gate_of<false>(t[e]);
-          }
-          if (p.scale) {
-            col8(p.scale, v * 8, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[j][e] *= w[e];
-          }
-          if (p.residual) {
-            r.get(t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[j][e] += t[e];
-          }
-          if (p.d_normed) {
-            en.get(ep[j]);
-            col8(p.w_pre, v * 8, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              P[j][e] = fmaf(ep[j][e], x[j][e] * rx, P[j][e]);
-              ep[j][e] *= w[e];
-              s = fmaf(ep[j][e], x[j][e], s);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ep[j][e] = 0.f;
-          }
-        }
-      }
+    const long long r = row0 + sub, base = r * p.dim + c;
+    const bool live = in && r < p.rows;
+    BwdRow<IO, GATE> row;
+    Raw<IO> u, z;
+    float s[3] = {0.f, 0.f, 0.f};
+    if (live) {
+      Raw<IO> res, dn, dout;
+      u.load(static_cast<const IO *>(p.u) + base);
+      if (GATE) z.load(static_cast<const IO *>(p.gate) + base);
+      if (p.residual) res.load(static_cast<const IO *>(p.residual) + base);
+      if (p.d_normed) dn.load(static_cast<const IO *>(p.d_normed) + base);
+      if (p.d_out) dout.load(static_cast<const IO *>(p.d_out) + base);
+      row.ru = p.w_post ? p.rstd_post[r] : 1.f;
+      row.rx = p.w_pre ? p.rstd_pre[r] : 0.f;
+      row.first(p, col, u, z, res, dn, dout, s);
     }
-    float cx = 0.f;
-    if (p.w_pre) cx = row_sum<LPR>(s, red, 0) * p.inv_dim * rx * rx * rx;
-    s = 0.f;
-    float dh[VPT][8], hat[VPT][8];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = lane + step * j;
-      if (live && v < nvec) {
-        Raw<IO> d;
-        float dx[8], w[8], t[8];
-        if (p.d_out) {
-          d.load(static_cast<const IO *>(p.d_out) + base + v * 8);
-          d.get(dx);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dx[e] = 0.f;
-        }
-        if (p.w_pre)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dx[e] += rx * ep[j][e] - x[j][e] * cx;
-        if (p.residual) store8(static_cast<IO *>(p.d_residual) + base + v * 8, dx);
-        u[j].get(hat[j]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) hat[j][e] *= ru;
-        float g[8];
-        if (p.gate) {
-          z[j].get(t);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float sg = gate_of<false>(t[e]);
-            g[e] = p.silu ? t[e] * sg : sg;
-            t[e] = p.silu ? sg * fmaf(t[e], 1.f - sg, 1.f) : sg * (1.f - sg);   // act'
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] = 1.f;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) A[j][e] = fmaf(dx[e], hat[j][e] * g[e], A[j][e]);
-        if (p.scale) {
-          col8(p.scale, v * 8, w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dx[e] *= w[e];
-        }
-        col8(p.w_post, v * 8, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          dx[e] *= w[e];
-          dh[j][e] = dx[e] * g[e];
-          s = fmaf(dh[j][e], hat[j][e], s);
-        }
-        if (p.gate) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) t[e] *= dx[e] * hat[j][e];
-          store8(static_cast<IO *>(p.d_gate) + base + v * 8, t);
-        }
-      }
-    }
-    float ch = 0.f;
-    if (p.w_post) ch = row_sum<LPR>(s, red, 1) * p.inv_dim;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = lane + step * j;
-      if (live && v < nvec) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dh[j][e] = ru * (dh[j][e] - hat[j][e] * ch);
-        store8(static_cast<IO *>(p.du) + base + v * 8, dh[j]);
-      }
-    }
-    // without both sums a set of `red` could be rewritten while another warp still reads it
-    if (LPR == 0 && !(p.w_pre && p.w_post)) __syncthreads();
+    for (int i = 0; i < 3; ++i) s[i] = row_sum<LPR>(s[i]);
+    if (live) row.second(p, col, u, z, s, base);
   }
-  if constexpr (LPR == 0) {
+  if (in)
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = lane + step * j;
-      if (v < nvec)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          p.partial[((size_t)blockIdx.x * 2) * p.dim + v * 8 + e] = A[j][e];
-          p.partial[((size_t)blockIdx.x * 2 + 1) * p.dim + v * 8 + e] = P[j][e];
-        }
+    for (int e = 0; e < 8; ++e) {
+      bn_smem[(size_t)sub * p.dim + c + e] = col.A[e];
+      bn_smem[(size_t)(rpc + sub) * p.dim + c + e] = col.P[e];
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = lane + step * j;
-      if (v < nvec)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          bn_smem[(size_t)sub * p.dim + v * 8 + e] = A[j][e];
-          bn_smem[(size_t)(rpc + sub) * p.dim + v * 8 + e] = P[j][e];
-        }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * p.dim; i += blockDim.x) {
-      const int which = i / p.dim, c = i - which * p.dim;
-      float t = 0.f;
-      for (int k = 0; k < rpc; ++k) t += bn_smem[(size_t)(which * rpc + k) * p.dim + c];
-      p.partial[((size_t)blockIdx.x * 2 + which) * p.dim + c] = t;
-    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * p.dim; i += blockDim.x) {
+    const int which = i / p.dim, col = i - which * p.dim;
+    float t = 0.f;
+    for (int k = 0; k < rpc; ++k) t += bn_smem[(size_t)(which * rpc + k) * p.dim + col];
+    p.partial[((size_t)blockIdx.x * 2 + which) * p.dim + col] = t;
   }
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_ranks() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(r));
+  return r;
+}
+// A row's three sums over a cluster. Inside a warp they are reduced together: after two halving steps lane
+// group g (8 lanes) holds value g, so six shuffles do. Every warp then sends its parts to every CTA of the
+// cluster by asynchronous stores that count on the receiver's barrier: no fence, which would wait for the
+// row's stores to global memory. red: [4][64] floats of the receiver, value by warp of the cluster.
+constexpr int SENT = 64;   // places per value: 8 CTAs x 8 warps
+__device__ __forceinline__ void send_sums(const float (&s)[3], float *red, uint64_t *bar, uint32_t rank, uint32_t ranks) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const bool up = lane & 16, up2 = lane & 8;
+  float a = up ? s[2] : s[0], b = up ? 0.f : s[1];   // values 2, 3 above lane 16, 0, 1 below
+  a += __shfl_xor_sync(0xffffffffu, up ? s[0] : s[2], 16);
+  b += __shfl_xor_sync(0xffffffffu, up ? s[1] : 0.f, 16);
+  float v = up2 ? b : a;
+  v += __shfl_xor_sync(0xffffffffu, up2 ? a : b, 8);
+#pragma unroll
+  for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((uint32_t)(lane & 7) < ranks) {
+    uint32_t d, m;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(d) : "r"(smem_u32(red + (lane >> 3) * SENT + rank * nw + warp)), "r"(lane & 7));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(m) : "r"(smem_u32(bar)), "r"(lane & 7));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];\n" ::"r"(d), "f"(v), "r"(m) : "memory");
+  }
+}
+__device__ __forceinline__ void take_sums(float (&s)[3], const float *red, uint32_t ranks) {
+  const int lane = threadIdx.x & 31, n = (int)(blockDim.x >> 5) * (int)ranks;
+  float v = 0.f;
+  for (int i = lane & 7; i < n; i += 8) v += red[(lane >> 3) * SENT + i];
+#pragma unroll
+  for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) s[i] = __shfl_sync(0xffffffffu, v, 8 * i);
+}
+
+// Long rows: a cluster of CTAs per row, each with 8 columns per thread. Persistent: cluster k of K takes
+// rows k, k + K, ...; the row's slices of the inputs arrive by bulk copies into a ring of p.stages buffers
+// (a row's buffer serves both its halves). A row's sums travel while the next row's first half is
+// computed. The two arrays of sums alternate: a CTA's parts of row i + 2 are sent after it has all parts
+// of row i + 1, and a warp sends those after it has read the sums of row i.
+template <typename IO, int GATE>
+__global__ void __launch_bounds__(256, 2) block_norm_bwd_kernel(BlockNormParams p) {
+  extern __shared__ __align__(128) char bn_ring[];
+  __shared__ float red[2][4 * SENT];
+  __shared__ __align__(8) uint64_t bar[6];   // 0..3 the ring, 4, 5 the sums
+  constexpr int VB = 8 * (int)sizeof(IO);   // bytes of a thread's columns
+  const uint32_t rank = cluster_rank(), ranks = cluster_ranks();
+  const int tid = threadIdx.x, nvec = p.dim >> 3, per = (nvec + (int)ranks - 1) / (int)ranks;
+  const int vbeg = (int)rank * per, own = min(per, nvec - vbeg);
+  const long long K = gridDim.x / ranks, k0 = blockIdx.x / ranks;
+  const bool in = tid < own;
+  const int c = (vbeg + (in ? tid : 0)) * 8;
+  const uint32_t slice = (uint32_t)own * VB, sent = 16u * ranks * (blockDim.x >> 5);
+  const int stride = per * VB, buffer = 5 * stride;   // a tensor's slice, a row's
+  if (tid == 0) {
+    for (int i = 0; i < 6; ++i) mbar_init(&bar[i], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  // every CTA's barriers exist before a peer's sums reach them
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  auto issue = [&](long long r, int b) {   // thread 0
+    const void *src[5] = {p.u, p.gate, p.residual, p.d_normed, p.d_out};
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) n += src[i] ? slice : 0u;
+    mbar_expect_tx(&bar[b], n);
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+      if (src[i]) bulk_g2s(bn_ring + b * buffer + i * stride, static_cast<const IO *>(src[i]) + r * p.dim + (size_t)vbeg * 8, slice, &bar[b]);
+  };
+  long long ahead = k0;   // the next row to ask for; two buffers are the current row's and the previous one's
+  if (tid == 0)
+    for (int i = 0; i < p.stages - 2 && ahead < p.rows; ++i, ahead += K) issue(ahead, i);
+  int fill = p.stages - 2;
+  BwdCols<IO> col(p, c);
+  BwdRow<IO, GATE> prev;
+  bool ok = true;
+  int b = 0, it = 0;
+  uint32_t phase = 0;
+  float ru = 1.f, rx = 0.f;
+  auto stats = [&](long long r) {   // loaded a row ahead
+    if (r < p.rows) {
+      if (p.w_post) ru = p.rstd_post[r];
+      if (p.w_pre) rx = p.rstd_pre[r];
+    }
+  };
+  auto finish = [&](long long r, int pb, int i) {   // the second half of row r = number i, in buffer pb
+    ok &= mbar_wait(&bar[4 + (i & 1)], (i >> 1) & 1);
+    float s[3];
+    take_sums(s, red[i & 1], ranks);
+    if (in) {
+      const char *buf = bn_ring + pb * buffer + (size_t)tid * VB;
+      Raw<IO> u, z;
+      u.loads(buf);
+      z.loads(buf + stride);
+      prev.second(p, col, u, z, s, r * p.dim + c);
+    }
+  };
+  stats(k0);
+  for (long long r = k0; r < p.rows; r += K, ++it) {
+    BwdRow<IO, GATE> row;
+    row.ru = ru, row.rx = rx;
+    stats(r + K);
+    ok &= mbar_wait(&bar[b], phase);   // on a timeout carry on to the end: the peers wait for the sums
+    float s[3] = {0.f, 0.f, 0.f};
+    if (in) {
+      const char *buf = bn_ring + b * buffer + (size_t)tid * VB;
+      Raw<IO> u, z, res, dn, dout;
+      u.loads(buf);
+      z.loads(buf + stride);
+      res.loads(buf + 2 * stride);
+      dn.loads(buf + 3 * stride);
+      dout.loads(buf + 4 * stride);
+      row.first(p, col, u, z, res, dn, dout, s);
+    }
+    if (it > 0) finish(r - K, b == 0 ? p.stages - 1 : b - 1, it - 1);
+    if (tid == 0) mbar_expect_tx(&bar[4 + (it & 1)], sent);
+    send_sums(s, red[it & 1], &bar[4 + (it & 1)], rank, ranks);
+    prev = row;
+    __syncthreads();   // the previous row's buffer is free
+    if (tid == 0 && ahead < p.rows) {
+      fence_proxy_async();
+      issue(ahead, fill);
+      ahead += K;
+    }
+    if (++fill == p.stages) fill = 0;
+    if (++b == p.stages) b = 0, phase ^= 1;
+  }
+  if (it > 0) finish(k0 + (long long)(it - 1) * K, b == 0 ? p.stages - 1 : b - 1, it - 1);
+  if (!ok) report(p.status, ERR_TIMEOUT);
+  if (in)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      p.partial[(size_t)k0 * 2 * p.dim + c + e] = col.A[e];
+      p.partial[((size_t)k0 * 2 + 1) * p.dim + c + e] = col.P[e];
+    }
 }
 
 // Column sums of the partials in a fixed order: 32 columns x 8 row groups per CTA, then the groups.
@@ -385,66 +523,123 @@ Shape shape(int dim) {
 }
 
 typedef void (*Kernel)(BlockNormParams);
-template <typename IO>
+template <typename IO, int GATE>
 Kernel fwd_fn(Shape s) {
   switch (s.lpr) {
-    case 1: return block_norm_fwd_kernel<IO, 1, 1>;
-    case 2: return block_norm_fwd_kernel<IO, 2, 1>;
-    case 4: return block_norm_fwd_kernel<IO, 4, 1>;
-    case 8: return block_norm_fwd_kernel<IO, 8, 1>;
-    case 16: return block_norm_fwd_kernel<IO, 16, 1>;
-    case 32: return block_norm_fwd_kernel<IO, 32, 1>;
+    case 1: return block_norm_fwd_kernel<IO, GATE, 1, 1>;
+    case 2: return block_norm_fwd_kernel<IO, GATE, 2, 1>;
+    case 4: return block_norm_fwd_kernel<IO, GATE, 4, 1>;
+    case 8: return block_norm_fwd_kernel<IO, GATE, 8, 1>;
+    case 16: return block_norm_fwd_kernel<IO, GATE, 16, 1>;
+    case 32: return block_norm_fwd_kernel<IO, GATE, 32, 1>;
   }
-  return s.vpt == 1 ? block_norm_fwd_kernel<IO, 0, 1> : s.vpt == 2 ? block_norm_fwd_kernel<IO, 0, 2> : block_norm_fwd_kernel<IO, 0, 4>;
+  return s.vpt == 1 ? block_norm_fwd_kernel<IO, GATE, 0, 1> : s.vpt == 2 ? block_norm_fwd_kernel<IO, GATE, 0, 2> : block_norm_fwd_kernel<IO, GATE, 0, 4>;
 }
-template <typename IO>
-Kernel bwd_fn(Shape s) {
-  switch (s.lpr) {
-    case 1: return block_norm_bwd_kernel<IO, 1, 1>;
-    case 2: return block_norm_bwd_kernel<IO, 2, 1>;
-    case 4: return block_norm_bwd_kernel<IO, 4, 1>;
-    case 8: return block_norm_bwd_kernel<IO, 8, 1>;
-    case 16: return block_norm_bwd_kernel<IO, 16, 1>;
-    case 32: return block_norm_bwd_kernel<IO, 32, 1>;
+template <typename IO, int GATE>
+Kernel bwd_fn(int lpr) {
+  switch (lpr) {
+    case 1: return block_norm_bwd_short_kernel<IO, GATE, 1>;
+    case 2: return block_norm_bwd_short_kernel<IO, GATE, 2>;
+    case 4: return block_norm_bwd_short_kernel<IO, GATE, 4>;
+    case 8: return block_norm_bwd_short_kernel<IO, GATE, 8>;
+    case 16: return block_norm_bwd_short_kernel<IO, GATE, 16>;
+    case 32: return block_norm_bwd_short_kernel<IO, GATE, 32>;
   }
-  return s.vpt == 1 ? block_norm_bwd_kernel<IO, 0, 1> : s.vpt == 2 ? block_norm_bwd_kernel<IO, 0, 2> : block_norm_bwd_kernel<IO, 0, 4>;
+  return block_norm_bwd_kernel<IO, GATE>;
 }
-size_t bwd_smem(Shape s, int dim) { return s.lpr ? (size_t)2 * (s.threads / s.lpr) * dim * sizeof(float) : 0; }
+int gate_kind(const BlockNormParams &p) { return p.gate ? (p.silu ? GATE_SILU : GATE_SIGMOID) : GATE_NONE; }
+Kernel fwd_fn(Shape s, int gate, bool f32) {
+  if (f32) return gate == GATE_NONE ? fwd_fn<float, GATE_NONE>(s) : gate == GATE_SILU ? fwd_fn<float, GATE_SILU>(s) : fwd_fn<float, GATE_SIGMOID>(s);
+  return gate == GATE_NONE ? fwd_fn<bf16, GATE_NONE>(s) : gate == GATE_SILU ? fwd_fn<bf16, GATE_SILU>(s) : fwd_fn<bf16, GATE_SIGMOID>(s);
+}
+Kernel bwd_fn(int lpr, int gate, bool f32) {
+  if (f32) return gate == GATE_NONE ? bwd_fn<float, GATE_NONE>(lpr) : gate == GATE_SILU ? bwd_fn<float, GATE_SILU>(lpr) : bwd_fn<float, GATE_SIGMOID>(lpr);
+  return gate == GATE_NONE ? bwd_fn<bf16, GATE_NONE>(lpr) : gate == GATE_SILU ? bwd_fn<bf16, GATE_SILU>(lpr) : bwd_fn<bf16, GATE_SIGMOID>(lpr);
+}
+
+// The backward's launch. Long rows: as few CTAs per row as 256 threads of 8 columns allow (1, 2, 4 or 8); four
+// buffers where they leave room for two CTAs per SM, else three. The count of CTAs sizes the workspace, so it
+// goes by the sizes alone: the gate's kernels are taken to hold as many at once as the SiLU's.
+struct BwdLaunch {
+  int lpr, threads, cluster, stages, ctas;   // ctas: rows of partials
+  size_t smem;
+};
+BwdLaunch bwd_launch(long long rows, int dim, bool f32) {
+  const Shape s = shape(dim);
+  BwdLaunch l{};
+  int dev = 0, sms = 0, at_once = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const Kernel fn = bwd_fn(s.lpr, GATE_SILU, f32);
+  long long groups;
+  if (s.lpr) {
+    const int rpc = s.threads / s.lpr;
+    l = {s.lpr, s.threads, 1, 0, 0, (size_t)2 * rpc * dim * sizeof(float)};
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&at_once, fn, l.threads, l.smem);
+    at_once *= sms;
+    groups = (rows + rpc - 1) / rpc;
+  } else {
+    const int nvec = dim / 8;
+    int cl = 1;
+    while (nvec > 256 * cl) cl *= 2;
+    const int per = (nvec + cl - 1) / cl;
+    const size_t buffer = (size_t)5 * per * 8 * (f32 ? 4 : 2);
+    const int stages = 4 * buffer <= 108 * 1024 ? 4 : 3;
+    l = {0, (per + 31) / 32 * 32, cl, stages, 0, stages * buffer};
+    for (int gate = GATE_NONE; gate <= GATE_SILU && e == cudaSuccess; ++gate)
+      e = cudaFuncSetAttribute(bwd_fn(0, gate, f32), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)l.smem);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cl;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)cl);
+    cfg.blockDim = dim3((unsigned)l.threads);
+    cfg.dynamicSmemBytes = l.smem;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&at_once, fn, &cfg);
+    groups = rows;
+  }
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    at_once = 152;
+  }
+  if (at_once < 1) at_once = 1;
+  l.ctas = (int)(groups < 1 ? 1 : (groups < at_once ? groups : at_once));
+  return l;
+}
 }  // namespace
 
-// Backward CTAs: as many as the device holds at once, at most one per row group.
-int block_norm_bwd_ctas(long long rows, int dim, bool f32) {
-  const Shape s = shape(dim);
-  const Kernel fn = f32 ? bwd_fn<float>(s) : bwd_fn<bf16>(s);
-  int dev = 0, sms = 0, per = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, fn, s.threads, bwd_smem(s, dim)) != cudaSuccess) {
-    (void)cudaGetLastError();
-    sms = 152, per = 1;
-  }
-  const long long most = (long long)sms * (per < 1 ? 1 : per);
-  const int rpc = s.lpr ? s.threads / s.lpr : 1;
-  const long long groups = (rows + rpc - 1) / rpc;
-  return (int)(groups < 1 ? 1 : (groups < most ? groups : most));
-}
+int block_norm_bwd_ctas(long long rows, int dim, bool f32) { return bwd_launch(rows, dim, f32).ctas; }
 
 cudaError_t launch_block_norm_fwd(const BlockNormParams &p, bool f32, cudaStream_t st) {
   if (p.rows == 0) return cudaSuccess;
   const Shape s = shape(p.dim);
   const int rpc = s.lpr ? s.threads / s.lpr : 1;
-  const Kernel fn = f32 ? fwd_fn<float>(s) : fwd_fn<bf16>(s);
+  const Kernel fn = fwd_fn(s, gate_kind(p), f32);
   fn<<<(unsigned)((p.rows + rpc - 1) / rpc), s.threads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_block_norm_bwd(const BlockNormParams &p, bool f32, cudaStream_t st) {
-  const Shape s = shape(p.dim);
-  const int ctas = block_norm_bwd_ctas(p.rows, p.dim, f32);
-  const Kernel fn = f32 ? bwd_fn<float>(s) : bwd_fn<bf16>(s);
-  fn<<<ctas, s.threads, bwd_smem(s, p.dim), st>>>(p);   // no rows: the partials become zero
-  cudaError_t e = cudaGetLastError();
+  const BwdLaunch l = bwd_launch(p.rows, p.dim, f32);
+  BlockNormParams q = p;
+  q.stages = l.stages;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)l.cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(l.ctas * l.cluster));
+  cfg.blockDim = dim3((unsigned)l.threads);
+  cfg.dynamicSmemBytes = l.smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, bwd_fn(l.lpr, gate_kind(p), f32), q);   // no rows: the partials become zero
   if (e != cudaSuccess) return e;
-  if (p.dw_post || p.dscale || p.dw_pre) block_norm_dw_kernel<<<(p.dim + 31) / 32, 256, 0, st>>>(p, ctas);
+  if (p.dw_post || p.dscale || p.dw_pre) block_norm_dw_kernel<<<(p.dim + 31) / 32, 256, 0, st>>>(p, l.ctas);
   return cudaGetLastError();
 }
 

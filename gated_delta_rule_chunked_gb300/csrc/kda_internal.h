@@ -280,8 +280,9 @@ struct BlockNormParams {
   const void *d_out, *d_normed;
   void *du, *d_gate, *d_residual;
   float *dw_post, *dscale, *dw_pre;
-  float *partial;              // [backward CTAs][2][dim]
+  float *partial;              // [backward CTAs or clusters][2][dim]
   int *status;
+  int stages;                  // backward, long rows: buffers of the ring (set by the launcher)
 };
 cudaError_t launch_block_norm_fwd(const BlockNormParams &p, bool f32, cudaStream_t s);
 cudaError_t launch_block_norm_bwd(const BlockNormParams &p, bool f32, cudaStream_t s);
