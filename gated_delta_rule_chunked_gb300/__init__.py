@@ -419,12 +419,21 @@ def kda_step(q, k, v, beta, g, state, accept_len=None, *, scale: float = 1.0, ou
 
 
 # ---------------------------------------------------------------- around the recurrent core
+# The current stream's handle without a Stream object around it, which would cost a small call several microseconds.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(device) -> int:
+    return _raw_stream(device.index) if _raw_stream is not None else _stream(device)
+
+
 def _need(t, name, dtype, shape, device):
-    """t as a contiguous CUDA tensor of this dtype and shape, or an exception that names it."""
-    if t.dtype != dtype:
+    """Address of t, a contiguous tensor of this dtype and shape on CUDA device number ``device``, or an
+    exception that names it."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {device}")
+    if t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on cuda:{device}")
     return t.data_ptr()
 
 
@@ -438,6 +447,8 @@ def _ints(t, name, n, device):
         return None
     if t.numel() != n:
         raise ValueError(f"{name} must have one entry per sequence")
+    if t.dtype is torch.int32 and t.get_device() == device.index and t.is_contiguous():
+        return t
     return t.to(device=device, dtype=torch.int32).contiguous()
 
 
@@ -445,13 +456,14 @@ def _rows(t, name, T, heads, dim, like):
     """Row stride of a [T, heads, dim] view whose rows are dense."""
     if t.dtype != like.dtype:
         raise TypeError(f"{name} must share x's dtype")
-    if t.shape != (T, heads, dim) or t.device != like.device:
+    if t.shape != (T, heads, dim) or t.get_device() != like.get_device():
         raise ValueError(f"{name} must be [{T}, {heads}, {dim}] on {like.device}")
-    if t.numel() == 0:
+    row, head, channel = t.stride()
+    if T == 0 or heads == 0:
         return heads * dim
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+    if channel != 1 or (heads > 1 and head != dim):
         raise ValueError(f"{name}'s rows must be dense (heads and channels side by side)")
-    return t.stride(0) if T > 1 else heads * dim
+    return row if T > 1 else heads * dim
 
 
 def ssm_fwd(x, dt, a, b, c, cu_seqlens=None, h0=None, *, d_skip=None, dt_bias=None, dt_softplus: bool = True,
@@ -466,27 +478,27 @@ def ssm_fwd(x, dt, a, b, c, cu_seqlens=None, h0=None, *, d_skip=None, dt_bias=No
     lib = library()
     if x.dim() != 3 or not x.is_cuda or b.dim() != 3:
         raise ValueError("x must be a CUDA tensor [T, H, P] and b [T, G, 128]")
-    dev = x.device
+    dev, di = x.device, x.get_device()
     (T, H, P), G = x.shape, b.shape[1]
-    cu = _i32(cu_seqlens, dev)
+    cu = cu_seqlens
+    if cu is not None and (cu.dtype is not torch.int32 or cu.get_device() != di or not cu.is_contiguous()):
+        cu = _i32(cu, dev)
     N = (cu.numel() - 1) if cu is not None else (n_seqs or 1)
     f32 = torch.float32
-    s = _lib.SsmArgs()
-    s.n_seqs, s.total_tokens, s.heads, s.groups, s.head_dim, s.d_state = N, T, H, G, P, b.shape[2]
-    s.io_dtype, s.dt_softplus = _io_dtype(x), int(dt_softplus)
-    s.cu_seqlens, s.x, s.b, s.c = _ptr(cu), x.data_ptr(), b.data_ptr(), c.data_ptr()
-    s.ldx, s.ldb, s.ldc = _rows(x, "x", T, H, P, x), _rows(b, "b", T, G, b.shape[2], x), _rows(c, "c", T, G, b.shape[2], x)
-    s.dt, s.a = _need(dt, "dt", f32, (T, H), dev), _need(a, "a", f32, (H,), dev)
-    s.dt_bias, s.d_skip = _maybe(dt_bias, "dt_bias", f32, (H,), dev), _maybe(d_skip, "d_skip", f32, (H,), dev)
-    s.h0 = _maybe(h0, "h0", f32, (N, H, b.shape[2], P), dev)
+    D = b.shape[2]
     y = torch.empty((T, H, P), dtype=x.dtype, device=dev)
-    hT = torch.empty((N, H, b.shape[2], P), dtype=f32, device=dev) if final_state else None
-    s.y, s.hT, s.dev_status = y.data_ptr(), _ptr(hT), _ptr(dev_status)
+    hT = torch.empty((N, H, D, P), dtype=f32, device=dev) if final_state else None
+    s = _lib.SsmArgs(
+        N, T, H, G, P, D, _io_dtype(x), int(dt_softplus), _ptr(cu), x.data_ptr(), b.data_ptr(), c.data_ptr(),
+        _rows(x, "x", T, H, P, x), _rows(b, "b", T, G, D, x), _rows(c, "c", T, G, D, x),
+        _need(dt, "dt", f32, (T, H), di), _need(a, "a", f32, (H,), di), _maybe(dt_bias, "dt_bias", f32, (H,), di),
+        _maybe(d_skip, "d_skip", f32, (H,), di), _maybe(h0, "h0", f32, (N, H, D, P), di), y.data_ptr(), _ptr(hT))
+    s.dev_status = _ptr(dev_status)
     ws_bytes = lib.kda_ssm_fwd_workspace_size(C.byref(s))
     if ws_bytes:
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         s.workspace, s.workspace_bytes = ws.data_ptr(), ws_bytes
-    _lib.check(lib.kda_ssm_fwd(C.byref(s), _stream(dev)))
+    _lib.check(lib.kda_ssm_fwd(C.byref(s), _stream_of(dev)))
     return y, hT
 
 
@@ -505,7 +517,7 @@ def ssm_step(xbc, dt, a, conv_weight, conv_bias, conv_state, state, accept_len=N
     lib = library()
     if xbc.dim() != 3 or not xbc.is_cuda or not xbc.is_contiguous() or state.dim() != 4 or conv_weight.dim() != 2:
         raise ValueError("xbc must be a contiguous CUDA tensor [N, L, C], state [slots, H, 128, P], conv_weight [C, W]")
-    dev, f32 = xbc.device, torch.float32
+    dev, di, f32 = xbc.device, xbc.get_device(), torch.float32
     N, L, Cc = xbc.shape
     slots, H, D, P = state.shape
     W = conv_weight.shape[1]
@@ -515,24 +527,18 @@ def ssm_step(xbc, dt, a, conv_weight, conv_bias, conv_state, state, accept_len=N
     first = _ints(first_slot, "first_slot", N, dev)
     if idx is None and slots != N:
         raise ValueError("state has one slot per sequence unless state_indices [N] addresses a pool")
-    s = _lib.SsmStepArgs()
-    s.n_seqs, s.steps, s.heads, s.groups, s.head_dim, s.d_state = N, L, H, groups, P, D
-    s.io_dtype, s.dt_softplus, s.width, s.activation = _io_dtype(xbc), int(dt_softplus), W, _ACT[activation]
-    s.xbc = xbc.data_ptr()
-    s.conv_weight = _need(conv_weight, "conv_weight", f32, (Cc, W), dev)
-    s.conv_bias = _maybe(conv_bias, "conv_bias", f32, (Cc,), dev)
-    if W > 1:
-        s.conv_state = _need(conv_state, "conv_state", xbc.dtype, (slots, W - 1, Cc), dev)
-    s.dt, s.a = _need(dt, "dt", f32, (N, L, H), dev), _need(a, "a", f32, (H,), dev)
-    s.dt_bias, s.d_skip = _maybe(dt_bias, "dt_bias", f32, (H,), dev), _maybe(d_skip, "d_skip", f32, (H,), dev)
-    s.state = _need(state, "state", f32, (slots, H, D, P), dev)
-    s.state_indices, s.accept_len, s.first_slot, s.n_slots = _ptr(idx), _ptr(acc), _ptr(first), slots
     y = torch.empty((N, L, H, P), dtype=xbc.dtype, device=dev) if out is None else out
-    s.y, s.dev_status = _need(y, "out", xbc.dtype, (N, L, H, P), dev), _ptr(dev_status)
-    ws_bytes = lib.kda_ssm_step_workspace_size(C.byref(s))
-    ws = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
-    s.workspace, s.workspace_bytes = ws.data_ptr(), ws_bytes
-    _lib.check(lib.kda_ssm_step(C.byref(s), _stream(dev)))
+    s = _lib.SsmStepArgs(
+        N, L, H, groups, P, D, _io_dtype(xbc), int(dt_softplus), W, _ACT[activation], xbc.data_ptr(),
+        _need(conv_weight, "conv_weight", f32, (Cc, W), di), _maybe(conv_bias, "conv_bias", f32, (Cc,), di),
+        _need(conv_state, "conv_state", xbc.dtype, (slots, W - 1, Cc), di) if W > 1 else None,
+        _need(dt, "dt", f32, (N, L, H), di), _need(a, "a", f32, (H,), di), _maybe(dt_bias, "dt_bias", f32, (H,), di),
+        _maybe(d_skip, "d_skip", f32, (H,), di), _need(state, "state", f32, (slots, H, D, P), di), _ptr(idx), _ptr(acc),
+        _ptr(first), slots, _need(y, "out", xbc.dtype, (N, L, H, P), di))
+    s.dev_status = _ptr(dev_status)
+    ws = torch.empty((N, L, Cc), dtype=f32, device=dev)   # the convolution's outputs: kda_ssm_step_workspace_size() bytes
+    s.workspace, s.workspace_bytes = ws.data_ptr(), 4 * N * L * Cc
+    _lib.check(lib.kda_ssm_step(C.byref(s), _stream_of(dev)))
     return y
 
 
@@ -551,19 +557,16 @@ def draft_verify(p, q, draft, u, noise, draft_len=None):
     lib = library()
     if p.dim() != 3 or not p.is_cuda:
         raise ValueError("p must be a CUDA tensor [N, L+1, V]")
-    dev, f32, i32 = p.device, torch.float32, torch.int32
+    dev, di, f32, i32 = p.device, p.get_device(), torch.float32, torch.int32
     N, L, V = p.shape[0], p.shape[1] - 1, p.shape[2]
-    s = _lib.DraftVerifyArgs()
-    s.n_seqs, s.drafts, s.vocab, s.io_dtype = N, L, V, _io_dtype(p)
-    s.p, s.q = _need(p, "p", p.dtype, (N, L + 1, V), dev), _maybe(q, "q", p.dtype, (N, L, V), dev)
-    s.draft, s.u = _need(draft, "draft", i32, (N, L), dev), _need(u, "u", f32, (N, L), dev)
-    s.noise = _need(noise, "noise", f32, (N, V), dev)
     lens = _ints(draft_len, "draft_len", N, dev)
-    s.draft_len = _ptr(lens)
     accept, first = torch.empty(N, dtype=i32, device=dev), torch.empty(N, dtype=i32, device=dev)
     tokens = torch.empty((N, L + 1), dtype=i32, device=dev)
-    s.accept_len, s.first_slot, s.tokens = accept.data_ptr(), first.data_ptr(), tokens.data_ptr()
-    _lib.check(lib.kda_draft_verify(C.byref(s), _stream(dev)))
+    s = _lib.DraftVerifyArgs(
+        N, L, V, _io_dtype(p), _need(p, "p", p.dtype, (N, L + 1, V), di), _maybe(q, "q", p.dtype, (N, L, V), di),
+        _need(draft, "draft", i32, (N, L), di), _ptr(lens), _need(u, "u", f32, (N, L), di),
+        _need(noise, "noise", f32, (N, V), di), accept.data_ptr(), first.data_ptr(), tokens.data_ptr())
+    _lib.check(lib.kda_draft_verify(C.byref(s), _stream_of(dev)))
     return accept, first, tokens
 
 
@@ -573,15 +576,13 @@ _GATE = {"sigmoid": _lib.KDA_GATE_SIGMOID, "silu": _lib.KDA_GATE_SILU}
 def _block_norm_args(u, w_post, gate, gate_act, residual, scale, w_pre, eps):
     if u.dim() < 1 or not u.is_cuda or not u.is_contiguous():
         raise ValueError("u must be a contiguous CUDA tensor [..., d]")
-    dev, d, f32 = u.device, u.shape[-1], torch.float32
-    n = _lib.BlockNormArgs()
-    n.rows, n.dim, n.eps, n.io_dtype = (u.numel() // d if d else 0), d, eps, _io_dtype(u)
-    n.gate_act = _GATE[gate_act]
-    n.u = u.data_ptr()
-    n.gate = _maybe(gate, "gate", u.dtype, u.shape, dev)
-    n.residual = _maybe(residual, "residual", u.dtype, u.shape, dev)
-    n.w_post, n.scale = _maybe(w_post, "w_post", f32, (d,), dev), _maybe(scale, "scale", f32, (d,), dev)
-    n.w_pre = _maybe(w_pre, "w_pre", f32, (d,), dev)
+    di, d, f32 = u.get_device(), u.shape[-1], torch.float32
+    shape = u.shape
+    n = _lib.BlockNormArgs(
+        u.numel() // d if d else 0, d, eps, _io_dtype(u), _GATE[gate_act], u.data_ptr(),
+        _maybe(gate, "gate", u.dtype, shape, di), _maybe(residual, "residual", u.dtype, shape, di),
+        _maybe(w_post, "w_post", f32, (d,), di), _maybe(scale, "scale", f32, (d,), di),
+        _maybe(w_pre, "w_pre", f32, (d,), di))
     return n
 
 
@@ -604,7 +605,7 @@ def block_norm_fwd(u, w_post, *, gate=None, gate_act: str = "silu", residual=Non
     rstd = lambda on: torch.empty(n.rows, dtype=torch.float32, device=u.device) if on is not None else None
     stats = (rstd(w_post), rstd(w_pre))
     n.out, n.normed, n.rstd_post, n.rstd_pre = out.data_ptr(), _ptr(normed), _ptr(stats[0]), _ptr(stats[1])
-    _lib.check(lib.kda_block_norm_fwd(C.byref(n), _stream(u.device)))
+    _lib.check(lib.kda_block_norm_fwd(C.byref(n), _stream_of(u.device)))
     return out, normed, stats
 
 
@@ -614,14 +615,14 @@ def block_norm_bwd(u, w_post, stats, d_out, d_normed=None, *, gate=None, gate_ac
     gradients of its two results, None for zero. Returns a dict: du, dgate, dresidual in u's
     dtype and dw_post, dscale, dw_pre fp32 [d], None where the input was absent."""
     lib = library()
-    dev, f32 = u.device, torch.float32
+    dev, di, f32 = u.device, u.get_device(), torch.float32
     b = _lib.BlockNormBwdArgs()
     b.fwd = _block_norm_args(u, w_post, gate, gate_act, residual, scale, w_pre, eps)
     rows, d = b.fwd.rows, b.fwd.dim
     for i, (name, w) in enumerate((("rstd_post", w_post), ("rstd_pre", w_pre))):
         if w is not None:
-            setattr(b.fwd, name, _need(stats[i], name, f32, (rows,), dev))
-    b.d_out, b.d_normed = _maybe(d_out, "d_out", u.dtype, u.shape, dev), _maybe(d_normed, "d_normed", u.dtype, u.shape, dev)
+            setattr(b.fwd, name, _need(stats[i], name, f32, (rows,), di))
+    b.d_out, b.d_normed = _maybe(d_out, "d_out", u.dtype, u.shape, di), _maybe(d_normed, "d_normed", u.dtype, u.shape, di)
     like = lambda t: None if t is None else torch.empty_like(u)
     vec = lambda t: None if t is None else torch.empty(d, dtype=f32, device=dev)
     g = {"du": torch.empty_like(u), "dgate": like(gate), "dresidual": like(residual), "dw_post": vec(w_post),
@@ -631,5 +632,5 @@ def block_norm_bwd(u, w_post, stats, d_out, d_normed=None, *, gate=None, gate_ac
     ws_bytes = lib.kda_block_norm_bwd_workspace_size(C.byref(b))
     ws = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
     b.workspace, b.workspace_bytes = ws.data_ptr(), ws_bytes
-    _lib.check(lib.kda_block_norm_bwd(C.byref(b), _stream(dev)))
+    _lib.check(lib.kda_block_norm_bwd(C.byref(b), _stream_of(dev)))
     return g

@@ -282,6 +282,7 @@ struct BlockNormParams {
   float *dw_post, *dscale, *dw_pre;
   float *partial;              // [backward CTAs or clusters][2][dim]
   int *status;
+  int prefetch_dist;           // forward, long rows: a CTA brings the row this far on into L2 (set by the launcher)
   int stages;                  // backward, long rows: buffers of the ring (set by the launcher)
 };
 cudaError_t launch_block_norm_fwd(const BlockNormParams &p, bool f32, cudaStream_t s);

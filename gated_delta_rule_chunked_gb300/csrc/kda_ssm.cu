@@ -3,11 +3,10 @@
 //
 //   h_t = softplus(dt_t + bias),  S_t = exp(h_t a) S_{t-1} + h_t B_t x_t^T,  y_t = S_t^T C_t + d x_t
 //
-// One CTA owns 64 value columns of one (sequence, head): 256 threads hold the 128 x 64 state in
-// registers, thread (g, q) rows 8 g .. 8 g + 7 and columns 4 q .. 4 q + 3 (the 16 lanes of a half
-// warp cover a row's 64 columns, so states move as whole 256-byte rows). Per token a thread reads
-// 8 values of B, 8 of C and 4 of h x from shared memory for 96 multiply-adds; the sums over the
-// 16 row groups meet once per 8 tokens.
+// One CTA owns 64 (or 16) value columns of one (sequence, head): 256 threads hold the 128 x 64 state in
+// registers, each 8 rows x 4 columns (16 lanes cover a row's 64 columns, so states move as whole 256-byte
+// rows). Per token a thread reads 8 values of B, 8 of C and 4 of x from shared memory for 96 operations;
+// the sums over the row groups meet once per 8 tokens.
 // Step: bound by reading and writing the 32 KB state. The convolution runs as a kernel of its own
 // (its state is shared by every head of a group, so it cannot be advanced in place by the heads'
 // CTAs), and the scan starts under it (programmatic dependent launch): it has its state in
@@ -18,105 +17,147 @@
 namespace kda {
 namespace {
 
-constexpr int TB = 8;   // tokens per batch (the step's most slots)
+constexpr int MAX_SLOTS = 8;   // of a step
 
 __device__ __forceinline__ float step_size(float v, bool softplus) {
   return softplus ? log1pf(expf(-fabsf(v))) + fmaxf(v, 0.f) : v;
 }
 
-struct RecSmem {
-  float x[TB][SSM_COLS], b[TB][SSM_N], c[TB][SSM_N];
-  float h[TB], dec[TB];
-  float yp[8][TB][SSM_COLS];   // per warp: sums over its rows
-};
+// W: value columns per CTA; TB: tokens per batch. A thread owns 4 columns of R rows: q = tid % (W / 4) says which columns, g = tid / (W / 4) which rows.
+template <int W, int TB>
+struct Rec {
+  static constexpr int Q = W / 4, G = 256 / Q, R = SSM_N / G;
+  typedef float State[R][4];
+  struct Smem {
+    float x[TB][W], b[TB][SSM_N], c[TB][SSM_N];
+    float h[TB], dec[TB];
+    float yp[8][TB][W];   // per warp: sums over its rows
+  };
 
-// `nt` tokens of the batch in `sm` through the state; commit(t) is called after token t.
-template <typename F>
-__device__ __forceinline__ void advance(RecSmem &sm, float (&S)[8][4], int t0, int nt, F commit) {
-  const int g = threadIdx.x >> 4, q = threadIdx.x & 15, warp = threadIdx.x >> 5;
-  for (int t = t0; t < nt; ++t) {
-    const float h = sm.h[t], dec = sm.dec[t];
-    float4 x = *reinterpret_cast<const float4 *>(&sm.x[t][4 * q]);
-    const float hx[4] = {h * x.x, h * x.y, h * x.z, h * x.w};
-    float b[8], c[8], y[4] = {0.f, 0.f, 0.f, 0.f};
-    *reinterpret_cast<float4 *>(b) = *reinterpret_cast<const float4 *>(&sm.b[t][8 * g]);
-    *reinterpret_cast<float4 *>(b + 4) = *reinterpret_cast<const float4 *>(&sm.b[t][8 * g + 4]);
-    *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(&sm.c[t][8 * g]);
-    *reinterpret_cast<float4 *>(c + 4) = *reinterpret_cast<const float4 *>(&sm.c[t][8 * g + 4]);
+  // Tokens t0 .. nt - 1 of the batch in `sm` through the state; commit(t) is called after token t. d x goes with the first
+  // rows' sums. (Two fp32 lanes per instruction take ten registers more at W = 64, and with them the fourth CTA of an SM.)
+  template <typename F>
+  static __device__ __forceinline__ void advance(Smem &sm, State &S, int t0, int nt, float d, F commit) {
+    const int g = threadIdx.x / Q, q = threadIdx.x % Q, warp = threadIdx.x >> 5;
+    const float dg = g == 0 ? d : 0.f;
+    for (int t = t0; t < nt; ++t) {
+      const float h = sm.h[t], dec = sm.dec[t];
+      const float4 x = *reinterpret_cast<const float4 *>(&sm.x[t][4 * q]);
+      const float hx[4] = {h * x.x, h * x.y, h * x.z, h * x.w};
+      float y[4] = {dg * x.x, dg * x.y, dg * x.z, dg * x.w};
+      constexpr int V = R < 4 ? R : 4;   // rows per read of B and C
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+      for (int j = 0; j < R; j += V) {
+        float b[V], c[V];
+        if constexpr (V == 4) {
+          *reinterpret_cast<float4 *>(b) = *reinterpret_cast<const float4 *>(&sm.b[t][R * g + j]);
+          *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(&sm.c[t][R * g + j]);
+        } else {
+          *reinterpret_cast<float2 *>(b) = *reinterpret_cast<const float2 *>(&sm.b[t][R * g + j]);
+          *reinterpret_cast<float2 *>(c) = *reinterpret_cast<const float2 *>(&sm.c[t][R * g + j]);
+        }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        S[i][k] = fmaf(S[i][k], dec, b[i] * hx[k]);
-        y[k] = fmaf(c[i], S[i][k], y[k]);
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float &s = S[j + i][k];
+            s = fmaf(s, dec, b[i] * hx[k]);
+            y[k] = fmaf(c[i], s, y[k]);
+          }
       }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] += __shfl_xor_sync(0xffffffffu, y[k], 16);
-    if ((threadIdx.x & 16) == 0) *reinterpret_cast<float4 *>(&sm.yp[warp][t][4 * q]) = make_float4(y[0], y[1], y[2], y[3]);
-    commit(t);
-  }
-}
-
-// The batch's outputs: the eight warps' sums in order, plus the skip.
-template <typename IO>
-__device__ __forceinline__ void put_y(const RecSmem &sm, int t0, int nt, float d, IO *y, long long ldy) {
-  for (int i = threadIdx.x; i < (nt - t0) * SSM_COLS; i += blockDim.x) {
-    const int t = t0 + i / SSM_COLS, p = i % SSM_COLS;
-    float v = d * sm.x[t][p];
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-    for (int w = 0; w < 8; ++w) v += sm.yp[w][t][p];
-    y[t * ldy + p] = from_f<IO>(v);
+        for (int o = Q; o < 32; o *= 2) y[k] += __shfl_xor_sync(0xffffffffu, y[k], o);
+      if ((threadIdx.x & 31) < Q) *reinterpret_cast<float4 *>(&sm.yp[warp][t][4 * q]) = make_float4(y[0], y[1], y[2], y[3]);
+      commit(t);
+    }
   }
-}
 
-__device__ __forceinline__ void load_state(const float *src, int P, float (&S)[8][4]) {
-  const int g = threadIdx.x >> 4, q = threadIdx.x & 15;
+  // The batch's outputs: the eight warps' sums in order.
+  template <typename IO>
+  static __device__ __forceinline__ void put_y(const Smem &sm, int t0, int nt, IO *y, long long ldy) {
+    for (int i = threadIdx.x; i < (nt - t0) * W; i += blockDim.x) {
+      const int t = t0 + i / W, p = i % W;
+      float v = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float4 v = src ? __ldcs(reinterpret_cast<const float4 *>(src + (size_t)(8 * g + i) * P + 4 * q)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    S[i][0] = v.x; S[i][1] = v.y; S[i][2] = v.z; S[i][3] = v.w;
+      for (int w = 0; w < 8; ++w) v += sm.yp[w][t][p];
+      y[t * ldy + p] = from_f<IO>(v);
+    }
   }
-}
-__device__ __forceinline__ void store_state(float *dst, int P, const float (&S)[8][4]) {
-  const int g = threadIdx.x >> 4, q = threadIdx.x & 15;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    __stcs(reinterpret_cast<float4 *>(dst + (size_t)(8 * g + i) * P + 4 * q), make_float4(S[i][0], S[i][1], S[i][2], S[i][3]));
-}
 
-// Prompts. Grid: (value slices of all heads, sequences).
+  static __device__ __forceinline__ void load_state(const float *src, int P, State &S) {
+    const int g = threadIdx.x / Q, q = threadIdx.x % Q;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float4 v = src ? __ldcs(reinterpret_cast<const float4 *>(src + (size_t)(R * g + i) * P + 4 * q)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      S[i][0] = v.x, S[i][1] = v.y, S[i][2] = v.z, S[i][3] = v.w;
+    }
+  }
+  static __device__ __forceinline__ void store_state(float *dst, int P, const State &S) {
+    const int g = threadIdx.x / Q, q = threadIdx.x % Q;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      __stcs(reinterpret_cast<float4 *>(dst + (size_t)(R * g + i) * P + 4 * q), make_float4(S[i][0], S[i][1], S[i][2], S[i][3]));
+  }
+};
+
+// Prompts. Grid: (slices of W value columns of all heads, sequences). The next batch's values are on their way while this
+// one's are used.
+template <int W, int TB>
 __global__ void __launch_bounds__(256) ssm_rec_kernel(SsmParams p) {
-  __shared__ __align__(16) RecSmem sm;
-  const int slices = p.P / SSM_COLS, head = blockIdx.x / slices, col0 = (blockIdx.x % slices) * SSM_COLS, n = blockIdx.y;
-  const int group = head / (p.H / p.G);
+  typedef Rec<W, TB> R;
+  __shared__ __align__(16) typename R::Smem sm;
+  const int slices = p.P / W, head = blockIdx.x / slices, col0 = (blockIdx.x % slices) * W, n = blockIdx.y;
+  const int group = head / (p.H / p.G), tid = threadIdx.x;
   const long long t0 = p.cu ? p.cu[n] : p.T / p.n_seqs * n, t1 = p.cu ? p.cu[n + 1] : p.T / p.n_seqs * (n + 1);
   const float *x = static_cast<const float *>(p.x) + (long long)head * p.P + col0;
   const float *b = static_cast<const float *>(p.b) + (long long)group * SSM_N, *c = static_cast<const float *>(p.c) + (long long)group * SSM_N;
   float *y = static_cast<float *>(p.y) + (long long)head * p.P + col0;
   const size_t soff = ((size_t)n * p.H + head) * SSM_N * p.P + col0;
   const float a = p.a[head], bias = p.dt_bias ? p.dt_bias[head] : 0.f, d = p.d_skip ? p.d_skip[head] : 0.f;
-  float S[8][4];
-  load_state(p.h0 ? p.h0 + soff : nullptr, p.P, S);
+  typename R::State S;
+  R::load_state(p.h0 ? p.h0 + soff : nullptr, p.P, S);
+  // thread: four values of B and of C of tokens tid / 32, tid / 32 + 8, ..., and (the first threads) four of x
+  constexpr int K = TB / 8;
+  float4 xv, bv[K], cv[K];
+  float dv;
+  const int bt = tid >> 5, be = (tid & 31) * 4, xt = tid / (W / 4), xe = tid % (W / 4) * 4;
+  auto fetch = [&](long long t) {
+    xv = make_float4(0.f, 0.f, 0.f, 0.f);
+    dv = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      bv[k] = cv[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t + bt + 8 * k < t1) {
+        bv[k] = *reinterpret_cast<const float4 *>(b + (t + bt + 8 * k) * p.ldb + be);
+        cv[k] = *reinterpret_cast<const float4 *>(c + (t + bt + 8 * k) * p.ldc + be);
+      }
+    }
+    if (xt < TB && t + xt < t1) xv = *reinterpret_cast<const float4 *>(x + (t + xt) * p.ldx + xe);
+    if (tid < TB && t + tid < t1) dv = p.dt[(t + tid) * p.H + head];
+  };
+  if (t0 < t1) fetch(t0);
   for (long long t = t0; t < t1; t += TB) {
     const int nt = (int)(t1 - t < TB ? t1 - t : TB);
-    __syncthreads();   // the previous batch is consumed
-    for (int i = threadIdx.x; i < nt * SSM_COLS; i += 256) sm.x[i / SSM_COLS][i % SSM_COLS] = (x[(t + i / SSM_COLS) * p.ldx + i % SSM_COLS]);
-    for (int i = threadIdx.x; i < nt * SSM_N; i += 256) {
-      const int k = i / SSM_N, e = i % SSM_N;
-      sm.b[k][e] = (b[(t + k) * p.ldb + e]);
-      sm.c[k][e] = (c[(t + k) * p.ldc + e]);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      *reinterpret_cast<float4 *>(&sm.b[bt + 8 * k][be]) = bv[k];
+      *reinterpret_cast<float4 *>(&sm.c[bt + 8 * k][be]) = cv[k];
     }
-    if ((int)threadIdx.x < nt) {
-      const float h = step_size(p.dt[(t + threadIdx.x) * p.H + head] + bias, p.softplus);
-      sm.h[threadIdx.x] = h;
-      sm.dec[threadIdx.x] = expf(h * a);
+    if (xt < TB) *reinterpret_cast<float4 *>(&sm.x[xt][xe]) = xv;
+    if (tid < TB) {
+      const float h = step_size(dv + bias, p.softplus);
+      sm.h[tid] = h;
+      sm.dec[tid] = expf(h * a);
     }
-    __syncthreads();
-    advance(sm, S, 0, nt, [](int) {});
-    __syncthreads();
-    put_y(sm, 0, nt, d, y + t * (long long)p.H * p.P, (long long)p.H * p.P);
+    __syncthreads();   // the batch is there; the previous one's outputs have been read
+    if (t + TB < t1) fetch(t + TB);
+    R::advance(sm, S, 0, nt, d, [](int) {});
+    __syncthreads();   // the batch is consumed, its sums are there
+    R::put_y(sm, 0, nt, y + t * (long long)p.H * p.P, (long long)p.H * p.P);
   }
-  if (p.hT) store_state(p.hT + soff, p.P, S);
+  if (p.hT) R::store_state(p.hT + soff, p.P, S);
 }
 
 // The convolution of the step: two channels per thread, all slots of one sequence. Grid:
@@ -185,8 +226,9 @@ __global__ void __launch_bounds__(256) ssm_conv_step_kernel(SsmParams p, int C) 
 
 // The scan of the step. Grid: (value slices of all heads, sequences).
 template <typename IO>
-__global__ void __launch_bounds__(256) ssm_step_kernel(SsmParams p, int C) {
-  __shared__ __align__(16) RecSmem sm;
+__global__ void __launch_bounds__(256, 4) ssm_step_kernel(SsmParams p, int C) {
+  typedef Rec<SSM_COLS, MAX_SLOTS> R;
+  __shared__ __align__(16) R::Smem sm;
   const int slices = p.P / SSM_COLS, head = blockIdx.x / slices, col0 = (blockIdx.x % slices) * SSM_COLS, n = blockIdx.y;
   const int slot = p.idx ? p.idx[n] : n;
   if (slot < 0 || slot >= p.n_slots) {
@@ -196,8 +238,8 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmParams p, int C) {
   const int group = head / (p.H / p.G), L = p.L;
   const int first = p.first ? min(max(p.first[n], 0), L) : 0, acc = p.acc ? min(max(p.acc[n], 0), L) : L;
   float *state = p.state + ((size_t)slot * p.H + head) * SSM_N * p.P + col0;
-  float S[8][4];
-  load_state(state, p.P, S);
+  R::State S;
+  R::load_state(state, p.P, S);
   if ((int)threadIdx.x < L) {
     const float h = step_size(p.dt[((size_t)n * L + threadIdx.x) * p.H + head] + (p.dt_bias ? p.dt_bias[head] : 0.f), p.softplus);
     sm.h[threadIdx.x] = h;
@@ -216,18 +258,25 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmParams p, int C) {
     *reinterpret_cast<float4 *>(&sm.c[t][e]) = __ldcg(reinterpret_cast<const float4 *>(c + (size_t)t * C + e));
   }
   __syncthreads();
-  advance(sm, S, first, L, [&](int t) {
-    if (t + 1 == acc) store_state(state, p.P, S);
+  R::advance(sm, S, first, L, p.d_skip ? p.d_skip[head] : 0.f, [&](int t) {
+    if (t + 1 == acc) R::store_state(state, p.P, S);
   });
   __syncthreads();
-  put_y(sm, first, L, p.d_skip ? p.d_skip[head] : 0.f,
-        static_cast<IO *>(p.y) + (size_t)n * L * p.H * p.P + (size_t)head * p.P + col0, (long long)p.H * p.P);
+  R::put_y(sm, first, L,
+           static_cast<IO *>(p.y) + (size_t)n * L * p.H * p.P + (size_t)head * p.P + col0, (long long)p.H * p.P);
 }
 
 }  // namespace
 
+// 64 columns per CTA do the least work per token (B and C are read by fewer threads); where that leaves the device mostly
+// empty, 16 columns take less time per token (512 tokens x 2 heads of 128: 86 us with 16 columns and 16 tokens per batch, 127 us with 64 and 8).
 cudaError_t launch_ssm_fwd_f32(const SsmParams &p, cudaStream_t s) {
-  ssm_rec_kernel<<<dim3(p.H * (p.P / SSM_COLS), p.n_seqs), 256, 0, s>>>(p);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  if ((long long)p.H * (p.P / 16) * p.n_seqs <= 2LL * sms) ssm_rec_kernel<16, 16><<<dim3(p.H * (p.P / 16), p.n_seqs), 256, 0, s>>>(p);
+  else ssm_rec_kernel<SSM_COLS, 8><<<dim3(p.H * (p.P / SSM_COLS), p.n_seqs), 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -69,19 +69,6 @@ enum Bar {
 };
 static_assert(NBAR <= SsmSmem::BARS, "a place for every barrier");
 
-// A bounded wait in few instructions: each try may suspend the warp for about a microsecond, so the
-// tries run out after about a second.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) {
-  uint32_t ok = 0;
-  for (uint32_t k = 0; k < (1u << 19) && !ok; ++k)
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-  return ok != 0;
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -134,47 +121,10 @@ __device__ __forceinline__ void commit(uint32_t leader, uint64_t *bar) {
       "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
 // The same box brought into L2 only.
 __device__ __forceinline__ void prefetch_2d(const CUtensorMap *map, int x, int y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y) : "memory");
 }
-// Two fp32 lanes per instruction.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 two(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 of2(f2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(a));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack2(f2 a) {
-  const float2 v = of2(a);
-  return pack2(v.x, v.y);
-}
-// The two bf16 of a word as fp32.
-__device__ __forceinline__ f2 unpack2(uint32_t w) { return two(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
 // Shared-memory descriptors (SWIZZLE_128B, 1024 bytes between 8-row groups) as their low word: the
 // high one is the same for all.
 __device__ __forceinline__ uint32_t dlo(uint32_t addr, uint32_t lbo) { return (addr & 0x3FFFF) >> 4 | (lbo >> 4) << 16; }
@@ -245,7 +195,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
         if (c > 0) {   // the previous chunk's Y, while this chunk's G runs
           const int k0 = c - 1, len = len_of(k0);
           char *ys = smem + (k0 & 1) * L::STAGE + L::X;   // in the place of the chunk's X, which everything has read by then
-          ok = wait(&bar[YDONE], k0 & 1) && wait(&bar[XEMPTY0 + (k0 & 1)], (k0 >> 1) & 1);
+          ok = mbar_wait_quiet(&bar[YDONE], k0 & 1) && mbar_wait_quiet(&bar[XEMPTY0 + (k0 & 1)], (k0 >> 1) & 1);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc::fence_after();
 #pragma unroll 1
@@ -273,7 +223,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
         }
         if (c == nch) break;
         // M's columns are free: the products of the previous chunk were issued before this G
-        ok = wait(&bar[SFULL], c & 1) && wait(&bar[GDONE], c & 1);
+        ok = mbar_wait_quiet(&bar[SFULL], c & 1) && mbar_wait_quiet(&bar[GDONE], c & 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc::fence_after();
         const float ci = sc_c[row];
@@ -332,12 +282,12 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
     // -------------------------------------------------------------- w o X
     for (c = 0; c < nch; ++c) {
       char *st = smem + (c & 1) * L::STAGE;
-      ok = ok && wait(&bar[SFULL], c & 1) && wait(&bar[XFULL0 + (c & 1)], (c >> 1) & 1);
+      ok = ok && mbar_wait_quiet(&bar[SFULL], c & 1) && mbar_wait_quiet(&bar[XFULL0 + (c & 1)], (c >> 1) & 1);
       if (!ok) break;
       const bool live = row < len_of(c);
       const float w = live ? sc_w[row] : 0.f;
       if (len_of(c) < Q) {
-        ok = wait(&bar[FULL0 + (c & 1)], (c >> 1) & 1);   // the only chunk at which this role waits for B: the sequence's last
+        ok = mbar_wait_quiet(&bar[FULL0 + (c & 1)], (c >> 1) & 1);   // the only chunk at which this role waits for B: the sequence's last
         if (!ok) break;
         if (!live) {   // rows past the sequence's end belong to another one, or to nobody: whatever they hold stays out
           const uint4 z = make_uint4(0u, 0u, 0u, 0u);
@@ -350,7 +300,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
         fence_proxy_async();
         mbar_arrive(&bar[TAIL]);
       }
-      if (c > 0) ok = wait(&bar[DSPART0 + wq], (c - 1) & 1);   // the previous terms of these tokens are read
+      if (c > 0) ok = mbar_wait_quiet(&bar[DSPART0 + wq], (c - 1) & 1);   // the previous terms of these tokens are read
       if (!ok) break;
       const f2 w2 = two(w, w), minus = two(-1.f, -1.f);
 #pragma unroll 1
@@ -418,14 +368,14 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
     if (!STATES) put();
     float log_dec = 0.f;
     for (c = 0; c < nch; ++c) {
-      ok = wait(&bar[SFULL], c & 1);
+      ok = mbar_wait_quiet(&bar[SFULL], c & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const float last = sc_c[Q - 1];
       mbar_arrive(&bar[SEMPTY]);
       const float dec = exp2f(last);
       const f2 dec2 = two(dec, dec);
       log_dec += last;
-      ok = wait(&bar[DSDONE], c & 1);
+      ok = mbar_wait_quiet(&bar[DSDONE], c & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::fence_after();
 #pragma unroll
@@ -442,7 +392,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
       tc::fence_before();
       mbar_arrive(&bar[DSFREE]);
       if (!STATES && c + 1 < nch) {
-        ok = wait(&bar[YDONE], c & 1);   // C S has read the previous operand
+        ok = mbar_wait_quiet(&bar[YDONE], c & 1);   // C S has read the previous operand
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         put();
       }
@@ -514,7 +464,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
         w[i] = h[i] * exp2f(suf[i] + ab);
       }
       // everything above ran beside the previous chunk; only the stores wait for its readers
-      if (c > 0) ok = wait(&bar[SEMPTY], (c - 1) & 1);
+      if (c > 0) ok = mbar_wait_quiet(&bar[SEMPTY], (c - 1) & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       *reinterpret_cast<float4 *>(sc_c + 4 * lane) = make_float4(pre[0], pre[1], pre[2], pre[3]);
       *reinterpret_cast<float4 *>(sc_h + 4 * lane) = make_float4(h[0], h[1], h[2], h[3]);
@@ -528,7 +478,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
       int issued = 0, xissued = 0;
       // chunk k's outputs leave as one box from the place of its X tile
       auto store = [&](int k) {
-        if (!wait(&bar[YSTAGED0 + (k & 1)], (k >> 1) & 1)) return false;
+        if (!mbar_wait_quiet(&bar[YSTAGED0 + (k & 1)], (k >> 1) & 1)) return false;
         if (len_of(k) == Q) {
           tma_store_2d(&p.tm_y, head * p.s.P + col0, t_begin + k * Q, smem + (k & 1) * L::STAGE + L::X);
           bulk_commit();
@@ -541,7 +491,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
         char *st = smem + (c & 1) * L::STAGE;
         const int t = t_begin + c * Q;
         if (c < nch) {   // B and C first: they are free before Y has left from X's place
-          if (c >= 2) ok = wait(&bar[EMPTY0 + (c & 1)], ((c >> 1) - 1) & 1);
+          if (c >= 2) ok = mbar_wait_quiet(&bar[EMPTY0 + (c & 1)], ((c >> 1) - 1) & 1);
           if (!ok) break;
           uint64_t *b = &bar[FULL0 + (c & 1)];
           mbar_expect_tx(b, STATES ? 32768 : 65536);
@@ -553,7 +503,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
             prefetch_2d(&p.tm_x, head * p.s.P + col0, t + Q);
           }
         }
-        if (c >= 2) ok = STATES ? wait(&bar[XEMPTY0 + (c & 1)], ((c >> 1) - 1) & 1) : store(c - 2);
+        if (c >= 2) ok = STATES ? mbar_wait_quiet(&bar[XEMPTY0 + (c & 1)], ((c >> 1) - 1) & 1) : store(c - 2);
         if (!ok) break;
         if (c < nch) {
           mbar_expect_tx(&bar[XFULL0 + (c & 1)], 16384);
@@ -563,9 +513,9 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
       }
       // every copy has landed, in either direction, before the CTA leaves, also after a timeout
 #pragma unroll 1
-      for (int k = issued > 2 ? issued - 2 : 0; k < issued; ++k) wait(&bar[FULL0 + (k & 1)], (k >> 1) & 1);
+      for (int k = issued > 2 ? issued - 2 : 0; k < issued; ++k) mbar_wait_quiet(&bar[FULL0 + (k & 1)], (k >> 1) & 1);
 #pragma unroll 1
-      for (int k = xissued > 2 ? xissued - 2 : 0; k < xissued; ++k) wait(&bar[XFULL0 + (k & 1)], (k >> 1) & 1);
+      for (int k = xissued > 2 ? xissued - 2 : 0; k < xissued; ++k) mbar_wait_quiet(&bar[XFULL0 + (k & 1)], (k >> 1) & 1);
       if (!STATES) bulk_wait_all();
     }
     __syncwarp();
@@ -579,7 +529,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
       for (c = 0; c < nch; ++c) {
         const uint32_t st = smem_u32(smem + (c & 1) * L::STAGE);
         const uint32_t d_c = dlo(st + L::C, 16), d_b = dlo(st + L::B, 16), d_x = dlo(st + L::X, 8192);
-        ok = wait(&bar[FULL0 + (c & 1)], (c >> 1) & 1) && (c == 0 || wait(&bar[GFREE], (c - 1) & 1)) && (len_of(c) == Q || wait(&bar[TAIL], 0));
+        ok = mbar_wait_quiet(&bar[FULL0 + (c & 1)], (c >> 1) & 1) && (c == 0 || mbar_wait_quiet(&bar[GFREE], (c - 1) & 1)) && (len_of(c) == Q || mbar_wait_quiet(&bar[TAIL], 0));
         if (!(ok = all(ok))) break;
         tc::fence_after();
 #pragma unroll
@@ -588,7 +538,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
           mma_ss(leader, tmem + T_G, desc(d_c + o), desc(d_b + o), tc::idesc_bf16(128, 128), ks > 0);
         }
         commit(leader, &bar[GDONE]);
-        ok = wait(&bar[SREADY], c & 1) && (c == 0 || wait(&bar[YFREE], (c - 1) & 1));
+        ok = mbar_wait_quiet(&bar[SREADY], c & 1) && (c == 0 || mbar_wait_quiet(&bar[YFREE], (c - 1) & 1));
         if (!(ok = all(ok))) break;
         tc::fence_after();
 #pragma unroll
@@ -596,10 +546,10 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
           mma_ss(leader, tmem + T_Y2, desc(d_c + (ks >> 2) * (16384 >> 4) + (ks & 3) * 2), desc(d_s + ks * (2048 >> 4)),
                  tc::idesc_bf16_mn(128, 64, false, true), ks > 0);
         commit(leader, &bar[EMPTY0 + (c & 1)]);
-        ok = wait(&bar[XFULL0 + (c & 1)], (c >> 1) & 1);
+        ok = mbar_wait_quiet(&bar[XFULL0 + (c & 1)], (c >> 1) & 1);
 #pragma unroll
         for (uint32_t k = 0; k < 4; ++k) {   // as M's column blocks become ready
-          ok = ok && all(wait(&bar[MREADY0 + k], c & 1));
+          ok = ok && all(mbar_wait_quiet(&bar[MREADY0 + k], c & 1));
           if (ok) {
             tc::fence_after();
             mma_ts(leader, tmem + T_Y1, tmem + T_M + 16 * k, desc(d_x + k * (4096 >> 4)), tc::idesc_bf16_mn(128, 64, false, true), k > 0);
@@ -610,7 +560,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
         commit(leader, &bar[YDONE]);
       }
       commit(leader, &bar[DRAIN0]);   // nothing of this thread runs on once the CTA leaves
-      ok &= wait(&bar[DRAIN0], 0);
+      ok &= mbar_wait_quiet(&bar[DRAIN0], 0);
     }
   } else {
     // -------------------------------------------------------------- B^T (w o X)
@@ -619,10 +569,10 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
 #pragma unroll 1
     for (c = 0; c < nch; ++c) {
       const uint32_t d_b = dlo(smem_u32(smem + (c & 1) * L::STAGE + L::B), 16384);
-      ok = wait(&bar[FULL0 + (c & 1)], (c >> 1) & 1) && (c == 0 || wait(&bar[DSFREE], (c - 1) & 1));
+      ok = mbar_wait_quiet(&bar[FULL0 + (c & 1)], (c >> 1) & 1) && (c == 0 || mbar_wait_quiet(&bar[DSFREE], (c - 1) & 1));
 #pragma unroll
       for (uint32_t k = 0; k < 4; ++k) {
-        ok = __all_sync(0xffffffffu, ok && wait(&bar[WXREADY0 + k], c & 1));
+        ok = __all_sync(0xffffffffu, ok && mbar_wait_quiet(&bar[WXREADY0 + k], c & 1));
         if (ok) {
           tc::fence_after();
           mma_ss(leader, tmem + T_DS, desc(d_b + k * (4096 >> 4)), desc(d_w + k * (4096 >> 4)), tc::idesc_bf16_mn(128, 192, true, true), k > 0);
@@ -636,7 +586,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
       commit(leader, &bar[EMPTY0 + (c & 1)]);
     }
     commit(leader, &bar[DRAIN1]);
-    ok &= wait(&bar[DRAIN1], 0);
+    ok &= mbar_wait_quiet(&bar[DRAIN1], 0);
   }
   if (!ok) report(p.s.status, ERR_TIMEOUT);
   tc::fence_before();
@@ -698,11 +648,17 @@ cudaError_t launch_ssm_fwd_tc(const SsmParams &s, int nseg, void *workspace, cud
   const size_t items = nseg > 1 ? (size_t)s.n_seqs * (nseg - 1) * U : 0;
   p.seg_state = static_cast<float *>(workspace);
   p.seg_decay = p.seg_state + items * SSM_N * SSM_COLS;
-  cudaError_t e = cudaFuncSetAttribute(ssm_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SsmSmem::BYTES);
+  // once per host thread and device: the kernels' shared memory
+  static thread_local int ready = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && ready != dev) {
+    e = cudaFuncSetAttribute(ssm_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SsmSmem::BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(ssm_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SsmSmem::BYTES);
+    if (e == cudaSuccess) ready = dev;
+  }
   if (e != cudaSuccess) return e;
   if (nseg > 1) {
-    e = cudaFuncSetAttribute(ssm_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SsmSmem::BYTES);
-    if (e != cudaSuccess) return e;
     ssm_tc_kernel<true><<<(unsigned)items, 896, SsmSmem::BYTES, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
