@@ -483,28 +483,29 @@ __global__ void __launch_bounds__(256, 2) block_norm_bwd_kernel(BlockNormParams 
     }
 }
 
-// Column sums of the partials in a fixed order: 32 columns x 8 row groups per CTA, then the groups.
-__global__ void __launch_bounds__(256) block_norm_dw_kernel(BlockNormParams p, int parts) {
-  __shared__ float sa[8][33], sp[8][33];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
-  float a = 0.f, b = 0.f;
+// Column sums of the partials in a fixed order: 32 columns x 32 row groups per CTA, then the groups. Launched under the
+// backward kernel's end.
+__global__ void __launch_bounds__(1024) block_norm_dw_kernel(BlockNormParams p, int parts) {
+  __shared__ float2 sums[32][33];
+  const int x = threadIdx.x & 31, c = blockIdx.x * 32 + x, g = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  float2 v = make_float2(0.f, 0.f);
   if (c < p.dim)
-    for (int k = g; k < parts; k += 8) {
-      a += p.partial[((size_t)k * 2) * p.dim + c];
-      b += p.partial[((size_t)k * 2 + 1) * p.dim + c];
+#pragma unroll 4
+    for (int k = g; k < parts; k += 32) {
+      v.x += __ldcg(&p.partial[((size_t)k * 2) * p.dim + c]);
+      v.y += __ldcg(&p.partial[((size_t)k * 2 + 1) * p.dim + c]);
     }
-  sa[g][threadIdx.x & 31] = a;
-  sp[g][threadIdx.x & 31] = b;
+  sums[g][x] = v;
   __syncthreads();
-  if (g == 0 && c < p.dim) {
-    a = b = 0.f;
-    for (int k = 0; k < 8; ++k) {
-      a += sa[k][threadIdx.x];
-      b += sp[k][threadIdx.x];
-    }
-    if (p.dw_post) p.dw_post[c] = a * (p.scale ? p.scale[c] : 1.f);
-    if (p.dscale) p.dscale[c] = a * (p.w_post ? p.w_post[c] : 1.f);
-    if (p.dw_pre) p.dw_pre[c] = b;
+  // warp g adds the groups of column g
+  v = sums[x][g];
+  v.x = row_sum<32>(v.x), v.y = row_sum<32>(v.y);
+  const int col = blockIdx.x * 32 + g;
+  if (x == 0 && col < p.dim) {
+    if (p.dw_post) p.dw_post[col] = v.x * (p.scale ? p.scale[col] : 1.f);
+    if (p.dscale) p.dscale[col] = v.x * (p.w_post ? p.w_post[col] : 1.f);
+    if (p.dw_pre) p.dw_pre[col] = v.y;
   }
 }
 
@@ -662,8 +663,13 @@ cudaError_t launch_block_norm_bwd(const BlockNormParams &p, bool f32, cudaStream
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, bwd_fn(l.lpr, gate_kind(p), f32), q);   // no rows: the partials become zero
   if (e != cudaSuccess) return e;
-  if (p.dw_post || p.dscale || p.dw_pre) block_norm_dw_kernel<<<(p.dim + 31) / 32, 256, 0, st>>>(p, l.ctas);
-  return cudaGetLastError();
+  if (!p.dw_post && !p.dscale && !p.dw_pre) return cudaSuccess;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)((p.dim + 31) / 32));
+  cfg.blockDim = dim3(1024);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, block_norm_dw_kernel, p, l.ctas);
 }
 
 }  // namespace kda

@@ -250,7 +250,7 @@ cudaError_t launch_ssm_fwd_f32(const SsmParams &p, cudaStream_t s);
 struct SsmTcParams {
   CUtensorMap tm_x, tm_b, tm_c, tm_y;   // [T][row], boxes of 64 columns x 128 tokens, 128-byte swizzle
   SsmParams s;
-  int nseg;
+  int nseg, sorted;   // sorted: CTAs take the sequences by falling length
   float *seg_state, *seg_decay;
 };
 int ssm_segments(int n_seqs, long long T, int units);

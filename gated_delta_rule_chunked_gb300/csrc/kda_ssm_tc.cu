@@ -132,6 +132,24 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo) { return (uint64_t)(64u | 
 // Byte offset of 16-byte chunk k of row r in a [rows][64] bf16 tile with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t row_chunk(int r, int k) { return (uint32_t)(r * 128 + ((k ^ (r & 7)) << 4)); }
 
+// Sequence number r of the sequences by falling length (at most MOST_SORTED, one thread each). CTAs start in the order of
+// their numbers, so the longest go first and none of them is left running alone at the end (eight packed prompts whose
+// longest is the last one: 0.211 -> 0.187 ms).
+constexpr int MOST_SORTED = 256;
+__device__ __forceinline__ int nth_longest(const int *cu, int n_seqs, int r, int *scratch) {
+  const int t = threadIdx.x;
+  if (t < n_seqs) scratch[t] = cu[t + 1] - cu[t];
+  __syncthreads();
+  if (t < n_seqs) {
+    const int len = scratch[t];
+    int rank = 0;
+    for (int j = 0; j < n_seqs; ++j) rank += scratch[j] > len || (scratch[j] == len && j < t);
+    if (rank == r) scratch[MOST_SORTED] = t;
+  }
+  __syncthreads();
+  return scratch[MOST_SORTED];
+}
+
 // STATES: the segments' own state contributions and decays only.
 template <bool STATES>
 __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ SsmTcParams p) {
@@ -144,7 +162,8 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, row = tid & 127;
   const int role = warp >> 3, half = (warp >> 2) & 1, wq = warp & 3;   // eight warps per role, two per 32 rows
   const int U = p.s.H * (p.s.P / SSM_COLS), nseg = p.nseg, runs = STATES ? nseg - 1 : nseg;
-  const int u = blockIdx.x % U, ns = blockIdx.x / U, seg = ns % runs, n = ns / runs;
+  const int u = blockIdx.x % U, ns = blockIdx.x / U, seg = ns % runs;
+  const int n = p.sorted ? nth_longest(p.s.cu, p.s.n_seqs, ns / runs, reinterpret_cast<int *>(smem)) : ns / runs;
   const int head = u / (p.s.P / SSM_COLS), col0 = (u % (p.s.P / SSM_COLS)) * SSM_COLS, group = head / (p.s.H / p.s.G);
   // token indices fit 32 bits (T < 2^31)
   const int each = (int)(p.s.T / p.s.n_seqs), seq0 = p.s.cu ? p.s.cu[n] : each * n, seq1 = p.s.cu ? p.s.cu[n + 1] : each * (n + 1);
@@ -636,6 +655,7 @@ cudaError_t launch_ssm_fwd_tc(const SsmParams &s, int nseg, void *workspace, cud
   SsmTcParams p{};
   p.s = s;
   p.nseg = nseg;
+  p.sorted = s.cu && s.n_seqs > 1 && s.n_seqs <= MOST_SORTED;
   const int U = s.H * (s.P / SSM_COLS);
   EncodeTiledFn fn = encode_tiled();
   if (!fn) return cudaErrorNotSupported;
