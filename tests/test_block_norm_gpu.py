@@ -136,6 +136,38 @@ def test_rows_of_zeros_and_large_values(kda, dim):
     assert (out[1] == 0).all() and (normed[1] == 0).all()
 
 
+def test_status_stays_clear_and_streams(kda):
+    s, grads, act = case(1500, 4096, "bf16", 9)
+    g = {k: cuda(v) for k, v in s.items()}
+    kw = dict(gate=g["gate"], gate_act=act, residual=g["residual"], scale=g["scale"], w_pre=g["w_pre"])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    do, dn = cuda(grads["d_out"]), cuda(grads["d_normed"])
+    _, _, stats = kda.block_norm_fwd(g["u"], g["w_post"], **kw)
+    a = kda.block_norm_bwd(g["u"], g["w_post"], stats, do, dn, dev_status=status, **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b = kda.block_norm_bwd(g["u"], g["w_post"], stats, do, dn, dev_status=status, **kw)
+    torch.cuda.current_stream().wait_stream(side)
+    assert int(status) == 0 and all(torch.equal(a[k], b[k]) for k in a)
+
+
+def test_captured_in_a_graph(kda):
+    s, grads, act = case(40, 1544, "bf16", 10)
+    g = {k: cuda(v) for k, v in s.items()}
+    kw = dict(gate=g["gate"], gate_act=act, residual=g["residual"], scale=g["scale"], w_pre=g["w_pre"])
+    do, dn = cuda(grads["d_out"]), cuda(grads["d_normed"])
+    run = lambda: (lambda f: (f, kda.block_norm_bwd(g["u"], g["w_post"], f[2], do, dn, **kw)))(kda.block_norm_fwd(g["u"], g["w_post"], **kw))
+    want = run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0][0], want[0][0]) and all(torch.equal(got[1][k], want[1][k]) for k in want[1])
+
+
 def test_same_call_same_bits(kda):
     s, grads, act = case(999, 1544, "bf16", 7)
     a, b = kernel(kda, s, act, grads=grads), kernel(kda, s, act, grads=grads)

@@ -173,6 +173,55 @@ def test_refusals(kda):
         kda.ssm_fwd(rows[:, :256].unflatten(1, (4, 64)), dt, a, b, c)
 
 
+@pytest.mark.parametrize("lens,H,G,P", [([2500], 1, 1, 64), ([2049, 1900], 1, 1, 128), ([3000, 0, 2, 2900], 1, 1, 64)])
+def test_long_prompts_in_segments(kda, lens, H, G, P):
+    """Few (sequence, head) pairs and many chunks: the sequences run in segments, folded from their own states."""
+    import ctypes as C
+    from gated_delta_rule_chunked_gb300 import _lib
+    a = _lib.SsmArgs()
+    a.n_seqs, a.total_tokens, a.heads, a.groups, a.head_dim, a.d_state = len(lens), sum(lens), H, G, P, 128
+    a.cu_seqlens = a.x = a.b = a.c = a.dt = a.a = a.y = 1 << 40
+    a.ldx, a.ldb, a.ldc = H * P, G * 128, G * 128
+    assert kda.library().kda_ssm_fwd_workspace_size(C.byref(a)) > 0          # a workspace is what segments need
+    check(kda, lens, H, G, P, "bf16", seed=sum(lens), strength=0.05)         # slow decay: the state crosses segments
+    check(kda, lens, H, G, P, "bf16", seed=sum(lens) + 1, h0=False)
+
+
+def test_many_sequences(kda):
+    """More sequences than are put in order of length, and more pairs than a wave."""
+    gen = torch.Generator().manual_seed(20)
+    lens = torch.randint(0, 12, (300,), generator=gen).tolist()
+    check(kda, lens, 2, 1, 64, "bf16", seed=21)
+    lens = torch.randint(0, 200, (40,), generator=gen).tolist()
+    check(kda, lens, 8, 4, 64, "bf16", seed=22)
+
+
+@pytest.mark.parametrize("N,H,P", [(1, 40, 128), (9, 5, 128), (3, 1, 64)])
+def test_fp32_slices(kda, N, H, P):
+    """fp32 prompts in slices of 64 and of 16 value columns."""
+    check(kda, [17] * N, H, 1, P, "f32", seed=N + H)
+
+
+@pytest.mark.parametrize("off", [8, 24])
+def test_rows_at_any_16_byte_offset(kda, off):
+    """x, B and C inside a wider row, at offsets that are multiples of 8 elements only."""
+    s = case([150], 2, 1, 64, "bf16", 30)
+    wide = torch.full((150, 384 + off + 16), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, off:off + 384] = s["rows"].cuda()
+    x, b, c = split(wide[:, off:off + 384], 2, 1, 64)
+    y, hT = kda.ssm_fwd(x, s["dt"].cuda(), s["a"].cuda(), b, c, None, s["h0"].cuda())
+    y_ref, h_ref = ref.scan(x, s["dt"], s["a"], b, c, [150], s["h0"])
+    assert ref.rel(y.float(), y_ref) <= TOL["bf16"] and ref.rel(hT, h_ref) <= TOL["f32"]
+
+
+def test_status_stays_clear(kda):
+    s = case([900, 300], 2, 1, 64, "bf16", 31)
+    x, b, c = split(s["rows"].cuda(), 2, 1, 64)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kda.ssm_fwd(x, s["dt"].cuda(), s["a"].cuda(), b, c, s["cu"].cuda(), dev_status=status)
+    assert int(status) == 0
+
+
 # ------------------------------------------------------------------------------------------ step
 def step_case(N, L, H, G, P, W, io, seed, pool=None):
     gen = torch.Generator().manual_seed(seed)
