@@ -174,54 +174,53 @@ __global__ void __launch_bounds__(256) ssm_conv_step_kernel(SsmParams p, int C) 
   }
   const int L = p.L, K = p.W - 1;   // K earlier inputs
   const int first = p.first ? min(max(p.first[n], 0), L) : 0, acc = p.acc ? min(max(p.acc[n], 0), L) : L;
+  IO *st = static_cast<IO *>(p.conv_state) + (size_t)slot * K * C + c;
+  const IO *x = static_cast<const IO *>(p.xbc) + (size_t)n * L * C + c;
+  float2 row[3 + MAX_SLOTS];   // K earlier inputs in rows 3 - K .. 2, then the slots; all on their way at once
+#pragma unroll
+  for (int j = 0; j < 3 + MAX_SLOTS; ++j) {
+    row[j] = make_float2(0.f, 0.f);
+    if (j < 3 ? j >= 3 - K : j - 3 >= first && j - 3 < L) row[j] = j < 3 ? ld2(st + (size_t)(j - (3 - K)) * C) : ld2(x + (size_t)(j - 3) * C);
+  }
   float w0[4], w1[4], win[4][2];   // right-aligned: tap 3 is the current token
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int k = j - (4 - p.W);
     w0[j] = k >= 0 ? p.cw[(size_t)c * p.W + k] : 0.f;
     w1[j] = k >= 0 ? p.cw[(size_t)(c + 1) * p.W + k] : 0.f;
-    win[j][0] = win[j][1] = 0.f;
+    win[j][0] = j < 3 ? row[j < 3 ? j : 0].x : 0.f;
+    win[j][1] = j < 3 ? row[j < 3 ? j : 0].y : 0.f;
   }
   const float b0 = p.cbias ? p.cbias[c] : 0.f, b1 = p.cbias ? p.cbias[c + 1] : 0.f;
-  IO *st = static_cast<IO *>(p.conv_state) + (size_t)slot * K * C + c;
-#pragma unroll
-  for (int j = 0; j < 3; ++j) {
-    const int k = j - (3 - K);
-    if (k >= 0) {
-      const float2 v = ld2(st + (size_t)k * C);
-      win[j][0] = v.x;
-      win[j][1] = v.y;
-    }
-  }
-  const IO *x = static_cast<const IO *>(p.xbc) + (size_t)n * L * C + c;
   float *out = p.conv + (size_t)n * L * C + c;
-  for (int s = first; s < L; ++s) {
-    const float2 v = ld2(x + (size_t)s * C);
-    win[3][0] = v.x;
-    win[3][1] = v.y;
-    float z0 = b0, z1 = b1;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      z0 = fmaf(w0[j], win[j][0], z0);
-      z1 = fmaf(w1[j], win[j][1], z1);
-    }
-    if (p.act) {
-      z0 = z0 / (1.f + expf(-z0));
-      z1 = z1 / (1.f + expf(-z1));
-    }
-    *reinterpret_cast<float2 *>(out + (size_t)s * C) = make_float2(z0, z1);
+  for (int s = 0; s < MAX_SLOTS; ++s)
+    if (s >= first && s < L) {
+      win[3][0] = row[3 + s].x;
+      win[3][1] = row[3 + s].y;
+      float z0 = b0, z1 = b1;
 #pragma unroll
-    for (int j = 0; j < 3; ++j) {
-      win[j][0] = win[j + 1][0];
-      win[j][1] = win[j + 1][1];
-    }
-    if (s + 1 == acc)
+      for (int j = 0; j < 4; ++j) {
+        z0 = fmaf(w0[j], win[j][0], z0);
+        z1 = fmaf(w1[j], win[j][1], z1);
+      }
+      if (p.act) {
+        z0 = __fdividef(z0, 1.f + __expf(-z0));   // a few units of 2^-23
+        z1 = __fdividef(z1, 1.f + __expf(-z1));
+      }
+      *reinterpret_cast<float2 *>(out + (size_t)s * C) = make_float2(z0, z1);
 #pragma unroll
       for (int j = 0; j < 3; ++j) {
-        const int k = j - (3 - K);
-        if (k >= 0) st2(st + (size_t)k * C, win[j][0], win[j][1]);
+        win[j][0] = win[j + 1][0];
+        win[j][1] = win[j + 1][1];
       }
-  }
+      if (s + 1 == acc)
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          const int k = j - (3 - K);
+          if (k >= 0) st2(st + (size_t)k * C, win[j][0], win[j][1]);
+        }
+    }
 }
 
 // The scan of the step. Grid: (value slices of all heads, sequences).
@@ -240,22 +239,31 @@ __global__ void __launch_bounds__(256, 4) ssm_step_kernel(SsmParams p, int C) {
   float *state = p.state + ((size_t)slot * p.H + head) * SSM_N * p.P + col0;
   R::State S;
   R::load_state(state, p.P, S);
-  if ((int)threadIdx.x < L) {
-    const float h = step_size(p.dt[((size_t)n * L + threadIdx.x) * p.H + head] + (p.dt_bias ? p.dt_bias[head] : 0.f), p.softplus);
-    sm.h[threadIdx.x] = h;
-    sm.dec[threadIdx.x] = expf(h * p.a[head]);
-  }
+  // the step sizes fall to the warp with the least to copy; everything is on its way before they are computed
+  const int tid = threadIdx.x, ht = tid - 224;
+  const bool steps = ht >= 0 && ht < L;
+  const float bias = p.dt_bias ? p.dt_bias[head] : 0.f, a = p.a[head];
+  const float dt = steps ? p.dt[((size_t)n * L + ht) * p.H + head] : 0.f;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the convolution's rows
   const float *rows = p.conv + (size_t)n * L * C;
   const float *x = rows + head * p.P + col0, *b = rows + p.H * p.P + group * SSM_N, *c = b + p.G * SSM_N;
-  for (int i = threadIdx.x; i < (L - first) * (SSM_COLS / 4); i += 256) {
-    const int t = first + i / (SSM_COLS / 4), e = i % (SSM_COLS / 4) * 4;
-    *reinterpret_cast<float4 *>(&sm.x[t][e]) = __ldcg(reinterpret_cast<const float4 *>(x + (size_t)t * C + e));
+  const int xt = tid >> 4, xe = (tid & 15) * 4, bt = tid >> 5, be = (tid & 31) * 4;   // one float4 each of x, B and C
+  float4 xv, bv, cv;
+  const bool xin = xt >= first && xt < L, bin = bt >= first && bt < L;
+  if (xin) xv = __ldcg(reinterpret_cast<const float4 *>(x + (size_t)xt * C + xe));
+  if (bin) {
+    bv = __ldcg(reinterpret_cast<const float4 *>(b + (size_t)bt * C + be));
+    cv = __ldcg(reinterpret_cast<const float4 *>(c + (size_t)bt * C + be));
   }
-  for (int i = threadIdx.x; i < (L - first) * (SSM_N / 4); i += 256) {
-    const int t = first + i / (SSM_N / 4), e = i % (SSM_N / 4) * 4;
-    *reinterpret_cast<float4 *>(&sm.b[t][e]) = __ldcg(reinterpret_cast<const float4 *>(b + (size_t)t * C + e));
-    *reinterpret_cast<float4 *>(&sm.c[t][e]) = __ldcg(reinterpret_cast<const float4 *>(c + (size_t)t * C + e));
+  if (steps) {
+    const float h = step_size(dt + bias, p.softplus);
+    sm.h[ht] = h;
+    sm.dec[ht] = expf(h * a);
+  }
+  if (xin) *reinterpret_cast<float4 *>(&sm.x[xt][xe]) = xv;
+  if (bin) {
+    *reinterpret_cast<float4 *>(&sm.b[bt][be]) = bv;
+    *reinterpret_cast<float4 *>(&sm.c[bt][be]) = cv;
   }
   __syncthreads();
   R::advance(sm, S, first, L, p.d_skip ? p.d_skip[head] : 0.f, [&](int t) {
