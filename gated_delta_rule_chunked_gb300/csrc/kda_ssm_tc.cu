@@ -2,8 +2,8 @@
 //
 // Chunks of 128 tokens. With c_i = sum_{k <= i} h_k a log2(e) over the chunk, S the state entering it:
 //   G  = C B^T                                              [128 x 128]
-//   M  = G o 2^(c_i - c_j) h_j  (j <= i, else 0) + d I
-//   Y  = M X + diag(2^c_i) C S
+//   M  = G o 2^(c_i - c_j) h_j  (j <= i, else 0)
+//   Y  = M X + diag(2^c_i) C S + d X
 //   S' = 2^c_last S + B^T (w o X),   w_j = 2^(sum_{k > j} h_k a log2 e) h_j
 // One CTA owns 64 value columns of one (sequence, head) and walks its chunks; the state stays in the
 // registers of one warpgroup (thread = state channel), so the chain between chunks is one multiply-add
@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
         tc::wait_st();
       }
       const float d = p.s.d_skip ? p.s.d_skip[head] : 0.f;
+      const f2 d2 = two(d, d);
       f2 e2 = two(0.f, 0.f);
       for (c = 0; c <= nch; ++c) {
         if (c > 0) {   // the previous chunk's Y, while this chunk's G runs
@@ -225,7 +226,15 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
             tc::ld16(tl + T_Y2 + 16 * k, u);
             tc::wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = pack2(fma2(e2, two(u[2 * i], u[2 * i + 1]), two(v[2 * i], v[2 * i + 1])));
+            for (int h = 0; h < 2; ++h) {
+              const uint4 xv = *reinterpret_cast<const uint4 *>(ys + row_chunk(row, 2 * k + h));
+              const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int j = 8 * h + 2 * i;
+                o[4 * h + i] = pack2(fma2(d2, unpack2(xw[i]), fma2(e2, two(u[j], u[j + 1]), two(v[j], v[j + 1]))));
+              }
+            }
             *reinterpret_cast<uint4 *>(ys + row_chunk(row, 2 * k)) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4 *>(ys + row_chunk(row, 2 * k + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
           }
@@ -277,15 +286,14 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
           tc::wait_ld();
           tc::fence_before();
           mbar_arrive(&bar[GFREE]);
-          const uint32_t keep = ((2u << lane) - 1u) >> (16 * half), diag = (1u << lane) >> (16 * half);   // columns j <= i, j = i
+          const uint32_t keep = ((2u << lane) - 1u) >> (16 * half);   // columns j <= i
           const f2 c2 = two(ci, ci), minus = two(-1.f, -1.f);
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
             const float2 cj = *reinterpret_cast<const float2 *>(sc_c + j0 + j), hj = *reinterpret_cast<const float2 *>(sc_h + j0 + j);
             const float2 x = of2(fma2(two(cj.x, cj.y), minus, c2));
             const float2 v = of2(mul2(mul2(two(ex2(x.x), ex2(x.y)), two(hj.x, hj.y)), two(g[j], g[j + 1])));
-            m[j / 2] = pack2(add2(two(keep >> j & 1u ? v.x : 0.f, keep >> (j + 1) & 1u ? v.y : 0.f),
-                                  two(diag >> j & 1u ? d : 0.f, diag >> (j + 1) & 1u ? d : 0.f)));
+            m[j / 2] = pack2(keep >> j & 1u ? v.x : 0.f, keep >> (j + 1) & 1u ? v.y : 0.f);
           }
           st8u(tl + T_M + j0 / 2, m);
           tc::wait_st();
