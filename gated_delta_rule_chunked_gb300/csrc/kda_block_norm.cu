@@ -477,12 +477,17 @@ __global__ void __launch_bounds__(256, 2) block_norm_bwd_kernel(BlockNormParams 
   }
   if (it > 0) finish(k0 + (long long)(it - 1) * K, b == 0 ? p.stages - 1 : b - 1, it - 1);
   if (!ok) report(p.status, ERR_TIMEOUT);
+  // no CTA leaves while sums are on their way to it, not even after a timeout
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
   if (in)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       *reinterpret_cast<float2 *>(&p.partial[(size_t)k0 * 2 * p.dim + c + 2 * e]) = of2(col.A[e]);
       *reinterpret_cast<float2 *>(&p.partial[((size_t)k0 * 2 + 1) * p.dim + c + 2 * e]) = of2(col.P[e]);
     }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
 // Column sums of the partials in a fixed order: 32 columns x 32 row groups per CTA, then the groups. Launched under the
@@ -567,6 +572,7 @@ Kernel bwd_fn(int lpr, int gate, bool full, bool f32) {
 // The backward's launch. Long rows: as few CTAs per row as 256 threads of 8 columns allow (1, 2, 4 or 8); three to
 // six buffers, as many as leave room for two CTAs per SM. The count of CTAs sizes the workspace, so it
 // goes by the sizes alone: the gate's kernels are taken to hold as many at once as the SiLU's.
+constexpr int BWD_RING = 3 * 5 * 256 * 8 * (int)sizeof(float);   // the largest ring: three rows of 256 threads' fp32 columns
 struct BwdLaunch {
   int lpr, threads, cluster, stages, ctas;   // ctas: rows of partials
   size_t smem;
@@ -603,11 +609,11 @@ BwdLaunch bwd_launch(long long rows, int dim, bool f32) {
     while (nvec > 256 * cl) cl *= 2;
     const int per = (nvec + cl - 1) / cl;
     const size_t buffer = (size_t)5 * per * 8 * (f32 ? 4 : 2);
-    int stages = (int)(108 * 1024 / buffer);
+    int stages = (int)(108 * 1024 / buffer);   // at most BWD_RING bytes, also where three take more
     stages = stages < 3 ? 3 : (stages > 6 ? 6 : stages);
     l = {0, (per + 31) / 32 * 32, cl, stages, 0, stages * buffer};
     for (int k = 0; ask && k < 6 && e == cudaSuccess; ++k)
-      e = cudaFuncSetAttribute(bwd_fn(0, k / 2, k % 2, f32), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)l.smem);
+      e = cudaFuncSetAttribute(bwd_fn(0, k / 2, k % 2, f32), cudaFuncAttributeMaxDynamicSharedMemorySize, BWD_RING);   // not l.smem: other sizes use the same kernels
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

@@ -205,3 +205,10 @@ def test_refusals(kda):
         kda.block_norm_fwd(u.half(), w)
     with pytest.raises(KeyError):
         kda.block_norm_fwd(u, w, gate=u, gate_act="relu")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_sizes_in_turn(kda, io):
+    # the sizes share kernels but not their shared memory: small ones between large ones change nothing
+    for dim in (7168, 2056, 16384, 264, 7168, 16384, 128, 2056):
+        check(kda, 5, dim, io, dim, **ALL)
