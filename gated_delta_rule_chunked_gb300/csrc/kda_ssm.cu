@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(256) ssm_rec_kernel(SsmParams p) {
   __shared__ __align__(16) typename R::Smem sm;
   const int slices = p.P / W, head = blockIdx.x / slices, col0 = (blockIdx.x % slices) * W, n = blockIdx.y;
   const int group = head / (p.H / p.G), tid = threadIdx.x;
-  const long long t0 = p.cu ? p.cu[n] : p.T / p.n_seqs * n, t1 = p.cu ? p.cu[n + 1] : p.T / p.n_seqs * (n + 1);
+  const long long t0 = max(p.cu ? (long long)p.cu[n] : p.T / p.n_seqs * n, 0LL), t1 = min(p.cu ? (long long)p.cu[n + 1] : p.T / p.n_seqs * (n + 1), p.T);
   const float *x = static_cast<const float *>(p.x) + (long long)head * p.P + col0;
   const float *b = static_cast<const float *>(p.b) + (long long)group * SSM_N, *c = static_cast<const float *>(p.c) + (long long)group * SSM_N;
   float *y = static_cast<float *>(p.y) + (long long)head * p.P + col0;

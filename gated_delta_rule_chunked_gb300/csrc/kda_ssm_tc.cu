@@ -166,7 +166,9 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
   const int n = p.sorted ? nth_longest(p.s.cu, p.s.n_seqs, ns / runs, reinterpret_cast<int *>(smem)) : ns / runs;
   const int head = u / (p.s.P / SSM_COLS), col0 = (u % (p.s.P / SSM_COLS)) * SSM_COLS, group = head / (p.s.H / p.s.G);
   // token indices fit 32 bits (T < 2^31)
-  const int each = (int)(p.s.T / p.s.n_seqs), seq0 = p.s.cu ? p.s.cu[n] : each * n, seq1 = p.s.cu ? p.s.cu[n + 1] : each * (n + 1);
+  // and offsets that are no sequence's are taken as an empty one
+  const int each = (int)(p.s.T / p.s.n_seqs), seq0 = max(p.s.cu ? p.s.cu[n] : each * n, 0);
+  const int seq1 = max(min(p.s.cu ? p.s.cu[n + 1] : each * (n + 1), (int)p.s.T), seq0);
   const int all = (int)(((unsigned)(seq1 - seq0) + Q - 1) / Q);
   const int first = (int)((long long)all * seg / nseg), nch = (int)((long long)all * (seg + 1) / nseg) - first;
   const int t_begin = seq0 + first * Q;
@@ -466,7 +468,11 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
       }
       float la[4], pre[4], suf[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) la[i] = h[i] * al;
+      for (int i = 0; i < 4; ++i) {
+        la[i] = h[i] * al;
+        // 2^-200 is zero in fp32 already: a token that forgets more would only cost the differences of the sums after it their digits
+        la[i] = la[i] < -200.f ? -200.f : la[i];
+      }
       pre[0] = la[0];
 #pragma unroll
       for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + la[i];

@@ -327,3 +327,34 @@ def test_step_refusals(kda):
         call(s["xbc"][:, :2], dt)                                                   # not contiguous
     with pytest.raises(TypeError):
         call(x, dt.half())
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("at", [0, 5, 100, 127, 200])
+def test_after_a_token_that_forgets_everything(kda, io, at):
+    # exp(h a) of one token is zero by a wide margin; what the tokens after it keep of one another is not touched by it
+    s = case([300], 2, 1, 64, io, 71)
+    s["a"] = torch.tensor([-0.5, -16.0])
+    s["dt"][at] = 1e5
+    s["rows"][at, :128] = 0   # its x
+    x, b, c = split(s["rows"].cuda(), 2, 1, 64)
+    y, hT = kda.ssm_fwd(x, s["dt"].cuda(), s["a"].cuda(), b, c, s["cu"], s["h0"].cuda(), d_skip=s["d_skip"].cuda(),
+                        dt_bias=s["dt_bias"].cuda())
+    y_ref, h_ref = ref.scan(x, s["dt"], s["a"], b, c, [300], s["h0"], s["d_skip"], s["dt_bias"])
+    for h in range(2):
+        assert ref.rel(y[at:, h].float(), torch.as_tensor(y_ref)[at:, h]) <= TOL[io]
+        assert ref.rel(hT[:, h], torch.as_tensor(h_ref)[:, h]) <= TOL["f32"]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_offsets_outside_the_tokens(kda, io):
+    # offsets past the last row end there; a falling pair is an empty sequence
+    s = case([40, 60, 30], 2, 1, 64, io, 72)
+    x, b, c = split(s["rows"].cuda(), 2, 1, 64)
+    call = lambda cu: kda.ssm_fwd(x, s["dt"].cuda(), s["a"].cuda(), b, c, torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                                  s["h0"].cuda(), d_skip=s["d_skip"].cuda(), dt_bias=s["dt_bias"].cuda())
+    y, hT = call([0, 40, 100, 130])
+    y1, hT1 = call([0, 40, 100, 500])
+    assert torch.equal(y, y1) and torch.equal(hT, hT1)
+    y2, hT2 = call([0, 40, 20, 130])   # the second is empty, the third starts at 20
+    assert torch.equal(hT2[1], s["h0"][1].cuda()) and torch.equal(hT2[0], hT[0])
