@@ -74,6 +74,75 @@ struct Rec {
     }
   }
 
+  // The whole batch, four tokens at a time and two columns per instruction: what a group reads from shared memory is on its way
+  // together, and its 16 sums over the lanes that share columns are taken side by side, half of the values handed over at each step.
+  static __device__ __forceinline__ void advance_batch(Smem &sm, const float *hs, const float *decs, f2 (&S)[R][2], float d) {
+    const int g = threadIdx.x / Q, q = threadIdx.x % Q, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool up = lane & 16, up2 = lane & 8, up4 = lane & 4;
+    const float dg = g == 0 ? d : 0.f;
+    constexpr int V = R < 4 ? R : 4;   // rows per read of B and C
+#pragma unroll 1
+    for (int t = 0; t < TB; t += 4) {
+      f2 x[4][2], y[4][2];
+      const float4 h4 = *reinterpret_cast<const float4 *>(hs + t), dec4 = *reinterpret_cast<const float4 *>(decs + t);
+      const float h[4] = {h4.x, h4.y, h4.z, h4.w}, dec[4] = {dec4.x, dec4.y, dec4.z, dec4.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = *reinterpret_cast<const float4 *>(&sm.x[t + i][4 * q]);
+        x[i][0] = two(v.x, v.y), x[i][1] = two(v.z, v.w);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) y[i][k] = mul2(two(dg, dg), x[i][k]), x[i][k] = mul2(two(h[i], h[i]), x[i][k]);
+      }
+#pragma unroll
+      for (int j = 0; j < R; j += V) {
+        float b[4][V], c[4][V];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (V == 4) {
+            *reinterpret_cast<float4 *>(b[i]) = *reinterpret_cast<const float4 *>(&sm.b[t + i][R * g + j]);
+            *reinterpret_cast<float4 *>(c[i]) = *reinterpret_cast<const float4 *>(&sm.c[t + i][R * g + j]);
+          } else {
+            *reinterpret_cast<float2 *>(b[i]) = *reinterpret_cast<const float2 *>(&sm.b[t + i][R * g + j]);
+            *reinterpret_cast<float2 *>(c[i]) = *reinterpret_cast<const float2 *>(&sm.c[t + i][R * g + j]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              f2 &s = S[j + v][k];
+              s = fma2(s, two(dec[i], dec[i]), mul2(two(b[i][v], b[i][v]), x[i][k]));
+              y[i][k] = fma2(two(c[i][v], c[i][v]), s, y[i][k]);
+            }
+      }
+      float u[4][4], z[2][4];   // tokens t + 2, t + 3 in the upper lanes, t, t + 1 in the lower ones
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = of2(y[i][0]), b = of2(y[i][1]);
+        u[i][0] = a.x, u[i][1] = a.y, u[i][2] = b.x, u[i][3] = b.y;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[i][k] = (up ? u[2 + i][k] : u[i][k]) + __shfl_xor_sync(0xffffffffu, up ? u[i][k] : u[2 + i][k], 16);
+      if constexpr (Q == 16) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<float4 *>(&sm.yp[warp][t + (up ? 2 : 0) + i][4 * q]) = make_float4(z[i][0], z[i][1], z[i][2], z[i][3]);
+      } else {
+        static_assert(Q == 4, "2 or 8 lanes to a column");
+        float v[4], o[2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = (up2 ? z[1][k] : z[0][k]) + __shfl_xor_sync(0xffffffffu, up2 ? z[0][k] : z[1][k], 8);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) o[k] = (up4 ? v[2 + k] : v[k]) + __shfl_xor_sync(0xffffffffu, up4 ? v[k] : v[2 + k], 4);
+        *reinterpret_cast<float2 *>(&sm.yp[warp][t + (up ? 2 : 0) + (up2 ? 1 : 0)][4 * q + (up4 ? 2 : 0)]) = make_float2(o[0], o[1]);
+      }
+    }
+  }
+
   // The batch's outputs: the eight warps' sums in order.
   template <typename IO>
   static __device__ __forceinline__ void put_y(const Smem &sm, int t0, int nt, IO *y, long long ldy) {
@@ -102,62 +171,98 @@ struct Rec {
   }
 };
 
-// Prompts. Grid: (slices of W value columns of all heads, sequences). The next batch's values are on their way while this
-// one's are used.
+// Prompts. Grid: (slices of W value columns of all heads, sequences); eight warps of the state, and a ninth for the next batch's step
+// sizes. The next batch's values are on their way while this one's are used.
 template <int W, int TB>
-__global__ void __launch_bounds__(256) ssm_rec_kernel(SsmParams p) {
+__global__ void __launch_bounds__(288) ssm_rec_kernel(SsmParams p) {
   typedef Rec<W, TB> R;
   __shared__ __align__(16) typename R::Smem sm;
+  __shared__ __align__(16) float steps[2][2][TB];   // by batch: h, exp(h a)
   const int slices = p.P / W, head = blockIdx.x / slices, col0 = (blockIdx.x % slices) * W, n = blockIdx.y;
-  const int group = head / (p.H / p.G), tid = threadIdx.x;
+  const int group = head / (p.H / p.G), tid = threadIdx.x, lane = tid & 31;
+  const bool scalars = tid >= 256;
   const long long t0 = max(p.cu ? (long long)p.cu[n] : p.T / p.n_seqs * n, 0LL), t1 = min(p.cu ? (long long)p.cu[n + 1] : p.T / p.n_seqs * (n + 1), p.T);
-  const float *x = static_cast<const float *>(p.x) + (long long)head * p.P + col0;
-  const float *b = static_cast<const float *>(p.b) + (long long)group * SSM_N, *c = static_cast<const float *>(p.c) + (long long)group * SSM_N;
-  float *y = static_cast<float *>(p.y) + (long long)head * p.P + col0;
   const size_t soff = ((size_t)n * p.H + head) * SSM_N * p.P + col0;
   const float a = p.a[head], bias = p.dt_bias ? p.dt_bias[head] : 0.f, d = p.d_skip ? p.d_skip[head] : 0.f;
   typename R::State S;
-  R::load_state(p.h0 ? p.h0 + soff : nullptr, p.P, S);
+  if (!scalars) R::load_state(p.h0 ? p.h0 + soff : nullptr, p.P, S);
+  f2 S2[R::R][2];
+#pragma unroll
+  for (int i = 0; i < R::R; ++i) S2[i][0] = two(S[i][0], S[i][1]), S2[i][1] = two(S[i][2], S[i][3]);
   // thread: four values of B and of C of tokens tid / 32, tid / 32 + 8, ..., and (the first threads) four of x
   constexpr int K = TB / 8;
   float4 xv, bv[K], cv[K];
-  float dv;
   const int bt = tid >> 5, be = (tid & 31) * 4, xt = tid / (W / 4), xe = tid % (W / 4) * 4;
-  auto fetch = [&](long long t) {
+  const float *x = static_cast<const float *>(p.x) + (t0 + xt) * p.ldx + (long long)head * p.P + col0 + xe;
+  const float *b = static_cast<const float *>(p.b) + (t0 + bt) * p.ldb + (long long)group * SSM_N + be;
+  const float *c = static_cast<const float *>(p.c) + (t0 + bt) * p.ldc + (long long)group * SSM_N + be;
+  const float *dt = p.dt + (t0 + lane) * p.H + head;
+  float *y = static_cast<float *>(p.y) + t0 * p.H * p.P + (long long)head * p.P + col0;
+  const long long ldy = (long long)p.H * p.P;
+  auto fetch = [&](int left) {   // of the batch that the pointers have reached, `left` tokens before the sequence's end; then past it
     xv = make_float4(0.f, 0.f, 0.f, 0.f);
-    dv = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       bv[k] = cv[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t + bt + 8 * k < t1) {
-        bv[k] = *reinterpret_cast<const float4 *>(b + (t + bt + 8 * k) * p.ldb + be);
-        cv[k] = *reinterpret_cast<const float4 *>(c + (t + bt + 8 * k) * p.ldc + be);
+      if (bt + 8 * k < left) {
+        bv[k] = *reinterpret_cast<const float4 *>(b + 8 * k * p.ldb);
+        cv[k] = *reinterpret_cast<const float4 *>(c + 8 * k * p.ldc);
       }
     }
-    if (xt < TB && t + xt < t1) xv = *reinterpret_cast<const float4 *>(x + (t + xt) * p.ldx + xe);
-    if (tid < TB && t + tid < t1) dv = p.dt[(t + tid) * p.H + head];
+    if (xt < TB && xt < left) xv = *reinterpret_cast<const float4 *>(x);
+    x += TB * p.ldx, b += TB * p.ldb, c += TB * p.ldc;
   };
-  if (t0 < t1) fetch(t0);
-  for (long long t = t0; t < t1; t += TB) {
-    const int nt = (int)(t1 - t < TB ? t1 - t : TB);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      *reinterpret_cast<float4 *>(&sm.b[bt + 8 * k][be]) = bv[k];
-      *reinterpret_cast<float4 *>(&sm.c[bt + 8 * k][be]) = cv[k];
-    }
-    if (xt < TB) *reinterpret_cast<float4 *>(&sm.x[xt][xe]) = xv;
-    if (tid < TB) {
+  float dv = 0.f;
+  auto fetch_dt = [&](int left) {
+    dv = lane < TB && lane < left ? *dt : 0.f;
+    dt += (long long)TB * p.H;
+  };
+  auto put_steps = [&](int which, int left) {   // past the end: tokens that leave the state as it is
+    if (lane < TB) {
       const float h = step_size(dv + bias, p.softplus);
-      sm.h[tid] = h;
-      sm.dec[tid] = expf(h * a);
+      steps[which][0][lane] = lane < left ? h : 0.f;
+      steps[which][1][lane] = lane < left ? expf(h * a) : 1.f;
+    }
+  };
+  int left = (int)(t1 > t0 ? t1 - t0 : 0), which = 0;
+  if (left > 0) {
+    if (scalars) {
+      fetch_dt(left);
+      put_steps(0, left);
+      fetch_dt(left - TB);
+    } else {
+      fetch(left);
+    }
+  }
+#pragma unroll 1
+  for (; left > 0; left -= TB, which ^= 1, y += TB * ldy) {
+    if (!scalars) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        *reinterpret_cast<float4 *>(&sm.b[bt + 8 * k][be]) = bv[k];
+        *reinterpret_cast<float4 *>(&sm.c[bt + 8 * k][be]) = cv[k];
+      }
+      if (xt < TB) *reinterpret_cast<float4 *>(&sm.x[xt][xe]) = xv;
     }
     __syncthreads();   // the batch is there; the previous one's outputs have been read
-    if (t + TB < t1) fetch(t + TB);
-    R::advance(sm, S, 0, nt, d, [](int) {});
+    if (scalars) {
+      put_steps(which ^ 1, left - TB);
+      fetch_dt(left - 2 * TB);
+    } else {
+      fetch(left - TB);
+      R::advance_batch(sm, steps[which][0], steps[which][1], S2, d);
+    }
     __syncthreads();   // the batch is consumed, its sums are there
-    R::put_y(sm, 0, nt, y + t * (long long)p.H * p.P, (long long)p.H * p.P);
+    R::put_y(sm, 0, left < TB ? left : TB, y, ldy);
   }
-  if (p.hT) R::store_state(p.hT + soff, p.P, S);
+  if (p.hT && !scalars) {
+#pragma unroll
+    for (int i = 0; i < R::R; ++i) {
+      const float2 v = of2(S2[i][0]), w = of2(S2[i][1]);
+      S[i][0] = v.x, S[i][1] = v.y, S[i][2] = w.x, S[i][3] = w.y;
+    }
+    R::store_state(p.hT + soff, p.P, S);
+  }
 }
 
 // The convolution of the step: two channels per thread, all slots of one sequence. Grid:
@@ -276,15 +381,16 @@ __global__ void __launch_bounds__(256, 4) ssm_step_kernel(SsmParams p, int C) {
 
 }  // namespace
 
-// 64 columns per CTA do the least work per token (B and C are read by fewer threads); where that leaves the device mostly
-// empty, 16 columns take less time per token (512 tokens x 2 heads of 128: 86 us with 16 columns and 16 tokens per batch, 127 us with 64 and 8).
+// 64 columns per CTA do the least work per token (B and C are read by fewer threads): 2048 tokens x 150 heads of 64 take 417 us.
+// Where that leaves the device mostly empty, 16 columns take less time per token: 512 tokens x 2 heads of 128 50 us, 98 ns a token,
+// most of it the issue of a token's products and sums.
 cudaError_t launch_ssm_fwd_f32(const SsmParams &p, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  if ((long long)p.H * (p.P / 16) * p.n_seqs <= 2LL * sms) ssm_rec_kernel<16, 16><<<dim3(p.H * (p.P / 16), p.n_seqs), 256, 0, s>>>(p);
-  else ssm_rec_kernel<SSM_COLS, 8><<<dim3(p.H * (p.P / SSM_COLS), p.n_seqs), 256, 0, s>>>(p);
+  if ((long long)p.H * (p.P / 16) * p.n_seqs <= 2LL * sms) ssm_rec_kernel<16, 16><<<dim3(p.H * (p.P / 16), p.n_seqs), 288, 0, s>>>(p);
+  else ssm_rec_kernel<SSM_COLS, 8><<<dim3(p.H * (p.P / SSM_COLS), p.n_seqs), 288, 0, s>>>(p);
   return cudaGetLastError();
 }
 
