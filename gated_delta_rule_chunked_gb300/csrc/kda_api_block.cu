@@ -119,7 +119,8 @@ kda::BlockNormParams norm_params(const kda_block_norm_args *a) {
 extern "C" {
 
 size_t kda_ssm_fwd_workspace_size(const kda_ssm_args *a) {
-  if (check_ssm(a, "kda_ssm_fwd_workspace_size") != KDA_OK || a->io_dtype == KDA_F32) return 0;
+  if (check_ssm(a, "kda_ssm_fwd_workspace_size") != KDA_OK) return 0;
+  if (a->io_dtype == KDA_F32) return kda::ssm_rec_plan(a->n_seqs, a->total_tokens, a->heads, a->head_dim).bytes;
   const int units = a->heads * (a->head_dim / kda::SSM_COLS);
   return kda::ssm_segment_bytes(a->n_seqs, units, kda::ssm_segments(a->n_seqs, a->total_tokens, units));
 }
@@ -129,11 +130,13 @@ kda_status kda_ssm_fwd(const kda_ssm_args *a, cudaStream_t stream) {
   const kda_status st = check_ssm(a, who);
   if (st != KDA_OK) return st;
   if (a->n_seqs == 0) return done(cudaSuccess, who);
-  if (a->io_dtype == KDA_F32) return done(kda::launch_ssm_fwd_f32(ssm_params(a), stream), who);
+  const bool f32 = a->io_dtype == KDA_F32;
+  const kda::SsmRecPlan rec = kda::ssm_rec_plan(a->n_seqs, a->total_tokens, a->heads, a->head_dim);
   const int units = a->heads * (a->head_dim / kda::SSM_COLS), nseg = kda::ssm_segments(a->n_seqs, a->total_tokens, units);
-  const size_t need = kda::ssm_segment_bytes(a->n_seqs, units, nseg);
+  const size_t need = f32 ? rec.bytes : kda::ssm_segment_bytes(a->n_seqs, units, nseg);
   if (need > 0 && (!have(a->workspace, 16) || a->workspace_bytes < need))
     return fail(KDA_ERR_INVALID_ARG, who, "workspace missing, misaligned or smaller than kda_ssm_fwd_workspace_size()");
+  if (f32) return done(kda::launch_ssm_fwd_f32(ssm_params(a), rec, a->workspace, stream), who);
   return done(kda::launch_ssm_fwd_tc(ssm_params(a), nseg, a->workspace, stream), who);
 }
 

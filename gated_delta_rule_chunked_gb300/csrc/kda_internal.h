@@ -244,7 +244,14 @@ struct SsmParams {
   float *state;
   const int *idx, *acc, *first;
 };
-cudaError_t launch_ssm_fwd_f32(const SsmParams &p, cudaStream_t s);
+// fp32 prompts: value columns per CTA and segments per sequence; the workspace holds the first nseg - 1 segments' state contributions
+// [N][nseg - 1][H P / cols][128][cols] and decays.
+struct SsmRecPlan {
+  int cols, nseg;
+  size_t bytes;
+};
+SsmRecPlan ssm_rec_plan(int n_seqs, long long T, int H, int P);
+cudaError_t launch_ssm_fwd_f32(const SsmParams &p, const SsmRecPlan &l, void *workspace, cudaStream_t s);
 // bf16 prompts on the tensor cores. Sequences run in nseg segments; the workspace holds the first
 // nseg - 1 segments' state contributions [N][nseg - 1][units][128][64] and decays.
 struct SsmTcParams {

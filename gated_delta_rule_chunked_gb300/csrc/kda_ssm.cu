@@ -76,6 +76,8 @@ struct Rec {
 
   // The whole batch, four tokens at a time and two columns per instruction: what a group reads from shared memory is on its way
   // together, and its 16 sums over the lanes that share columns are taken side by side, half of the values handed over at each step.
+  // Without OUT only the state moves.
+  template <bool OUT>
   static __device__ __forceinline__ void advance_batch(Smem &sm, const float *hs, const float *decs, f2 (&S)[R][2], float d) {
     const int g = threadIdx.x / Q, q = threadIdx.x % Q, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool up = lane & 16, up2 = lane & 8, up4 = lane & 4;
@@ -100,10 +102,10 @@ struct Rec {
         for (int i = 0; i < 4; ++i) {
           if constexpr (V == 4) {
             *reinterpret_cast<float4 *>(b[i]) = *reinterpret_cast<const float4 *>(&sm.b[t + i][R * g + j]);
-            *reinterpret_cast<float4 *>(c[i]) = *reinterpret_cast<const float4 *>(&sm.c[t + i][R * g + j]);
+            if (OUT) *reinterpret_cast<float4 *>(c[i]) = *reinterpret_cast<const float4 *>(&sm.c[t + i][R * g + j]);
           } else {
             *reinterpret_cast<float2 *>(b[i]) = *reinterpret_cast<const float2 *>(&sm.b[t + i][R * g + j]);
-            *reinterpret_cast<float2 *>(c[i]) = *reinterpret_cast<const float2 *>(&sm.c[t + i][R * g + j]);
+            if (OUT) *reinterpret_cast<float2 *>(c[i]) = *reinterpret_cast<const float2 *>(&sm.c[t + i][R * g + j]);
           }
         }
 #pragma unroll
@@ -114,9 +116,10 @@ struct Rec {
             for (int k = 0; k < 2; ++k) {
               f2 &s = S[j + v][k];
               s = fma2(s, two(dec[i], dec[i]), mul2(two(b[i][v], b[i][v]), x[i][k]));
-              y[i][k] = fma2(two(c[i][v], c[i][v]), s, y[i][k]);
+              if (OUT) y[i][k] = fma2(two(c[i][v], c[i][v]), s, y[i][k]);
             }
       }
+      if (!OUT) continue;
       float u[4][4], z[2][4];   // tokens t + 2, t + 3 in the upper lanes, t, t + 1 in the lower ones
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -172,23 +175,38 @@ struct Rec {
 };
 
 // Prompts. Grid: (slices of W value columns of all heads, sequences); eight warps of the state, and a ninth for the next batch's step
-// sizes. The next batch's values are on their way while this one's are used.
-template <int W, int TB>
-__global__ void __launch_bounds__(288) ssm_rec_kernel(SsmParams p) {
+// sizes. The next batch's values are on their way while this one's are used. Sequences run in nseg segments of whole batches: STATES
+// finds what each but the last adds to the state, and its decay; then every segment starts from what those before it make of h0.
+template <int W, int TB, bool STATES>
+__global__ void __launch_bounds__(288) ssm_rec_kernel(SsmParams p, int nseg, float *seg_state, float *seg_decay) {
   typedef Rec<W, TB> R;
   __shared__ __align__(16) typename R::Smem sm;
   __shared__ __align__(16) float steps[2][2][TB];   // by batch: h, exp(h a)
-  const int slices = p.P / W, head = blockIdx.x / slices, col0 = (blockIdx.x % slices) * W, n = blockIdx.y;
+  const int slices = p.P / W, head = blockIdx.x / slices, col0 = (blockIdx.x % slices) * W;
+  const int runs = STATES ? nseg - 1 : nseg, n = blockIdx.y / runs, seg = blockIdx.y % runs;
   const int group = head / (p.H / p.G), tid = threadIdx.x, lane = tid & 31;
   const bool scalars = tid >= 256;
-  const long long t0 = max(p.cu ? (long long)p.cu[n] : p.T / p.n_seqs * n, 0LL), t1 = min(p.cu ? (long long)p.cu[n + 1] : p.T / p.n_seqs * (n + 1), p.T);
+  const long long seq0 = max(p.cu ? (long long)p.cu[n] : p.T / p.n_seqs * n, 0LL), seq1 = min(p.cu ? (long long)p.cu[n + 1] : p.T / p.n_seqs * (n + 1), p.T);
+  const long long batches = seq1 > seq0 ? (seq1 - seq0 + TB - 1) / TB : 0;
+  const long long t0 = seq0 + batches * seg / nseg * TB, t1 = min(seq1, seq0 + batches * (seg + 1) / nseg * TB);
   const size_t soff = ((size_t)n * p.H + head) * SSM_N * p.P + col0;
   const float a = p.a[head], bias = p.dt_bias ? p.dt_bias[head] : 0.f, d = p.d_skip ? p.d_skip[head] : 0.f;
   typename R::State S;
-  if (!scalars) R::load_state(p.h0 ? p.h0 + soff : nullptr, p.P, S);
+  if (!scalars) R::load_state(!STATES && p.h0 ? p.h0 + soff : nullptr, p.P, S);
   f2 S2[R::R][2];
 #pragma unroll
   for (int i = 0; i < R::R; ++i) S2[i][0] = two(S[i][0], S[i][1]), S2[i][1] = two(S[i][2], S[i][3]);
+  if (!STATES && !scalars)
+    for (int k = 0; k < seg; ++k) {
+      const size_t at = ((size_t)n * (nseg - 1) + k) * gridDim.x + blockIdx.x;
+      const float dec = seg_decay[at];
+      R::load_state(seg_state + at * SSM_N * W, W, S);
+#pragma unroll
+      for (int i = 0; i < R::R; ++i) {
+        S2[i][0] = fma2(S2[i][0], two(dec, dec), two(S[i][0], S[i][1]));
+        S2[i][1] = fma2(S2[i][1], two(dec, dec), two(S[i][2], S[i][3]));
+      }
+    }
   // thread: four values of B and of C of tokens tid / 32, tid / 32 + 8, ..., and (the first threads) four of x
   constexpr int K = TB / 8;
   float4 xv, bv[K], cv[K];
@@ -206,13 +224,13 @@ __global__ void __launch_bounds__(288) ssm_rec_kernel(SsmParams p) {
       bv[k] = cv[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (bt + 8 * k < left) {
         bv[k] = *reinterpret_cast<const float4 *>(b + 8 * k * p.ldb);
-        cv[k] = *reinterpret_cast<const float4 *>(c + 8 * k * p.ldc);
+        if (!STATES) cv[k] = *reinterpret_cast<const float4 *>(c + 8 * k * p.ldc);
       }
     }
     if (xt < TB && xt < left) xv = *reinterpret_cast<const float4 *>(x);
     x += TB * p.ldx, b += TB * p.ldb, c += TB * p.ldc;
   };
-  float dv = 0.f;
+  float dv = 0.f, log_dec = 0.f;
   auto fetch_dt = [&](int left) {
     dv = lane < TB && lane < left ? *dt : 0.f;
     dt += (long long)TB * p.H;
@@ -220,6 +238,7 @@ __global__ void __launch_bounds__(288) ssm_rec_kernel(SsmParams p) {
   auto put_steps = [&](int which, int left) {   // past the end: tokens that leave the state as it is
     if (lane < TB) {
       const float h = step_size(dv + bias, p.softplus);
+      if (lane < left) log_dec += h * a;
       steps[which][0][lane] = lane < left ? h : 0.f;
       steps[which][1][lane] = lane < left ? expf(h * a) : 1.f;
     }
@@ -240,7 +259,7 @@ __global__ void __launch_bounds__(288) ssm_rec_kernel(SsmParams p) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         *reinterpret_cast<float4 *>(&sm.b[bt + 8 * k][be]) = bv[k];
-        *reinterpret_cast<float4 *>(&sm.c[bt + 8 * k][be]) = cv[k];
+        if (!STATES) *reinterpret_cast<float4 *>(&sm.c[bt + 8 * k][be]) = cv[k];
       }
       if (xt < TB) *reinterpret_cast<float4 *>(&sm.x[xt][xe]) = xv;
     }
@@ -250,18 +269,25 @@ __global__ void __launch_bounds__(288) ssm_rec_kernel(SsmParams p) {
       fetch_dt(left - 2 * TB);
     } else {
       fetch(left - TB);
-      R::advance_batch(sm, steps[which][0], steps[which][1], S2, d);
+      R::template advance_batch<!STATES>(sm, steps[which][0], steps[which][1], S2, d);
     }
     __syncthreads();   // the batch is consumed, its sums are there
-    R::put_y(sm, 0, left < TB ? left : TB, y, ldy);
+    if (!STATES) R::put_y(sm, 0, left < TB ? left : TB, y, ldy);
   }
-  if (p.hT && !scalars) {
+  const size_t at = ((size_t)n * (nseg - 1) + seg) * gridDim.x + blockIdx.x;
+  if (STATES && scalars) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) log_dec += __shfl_xor_sync(0xffffffffu, log_dec, o);
+    if (lane == 0) seg_decay[at] = expf(log_dec);
+  }
+  if (!scalars && (STATES || (p.hT && seg == nseg - 1))) {
 #pragma unroll
     for (int i = 0; i < R::R; ++i) {
       const float2 v = of2(S2[i][0]), w = of2(S2[i][1]);
       S[i][0] = v.x, S[i][1] = v.y, S[i][2] = w.x, S[i][3] = w.y;
     }
-    R::store_state(p.hT + soff, p.P, S);
+    if (STATES) R::store_state(seg_state + at * SSM_N * W, W, S);
+    else R::store_state(p.hT + soff, p.P, S);
   }
 }
 
@@ -381,17 +407,51 @@ __global__ void __launch_bounds__(256, 4) ssm_step_kernel(SsmParams p, int C) {
 
 }  // namespace
 
-// 64 columns per CTA do the least work per token (B and C are read by fewer threads): 2048 tokens x 150 heads of 64 take 417 us.
-// Where that leaves the device mostly empty, 16 columns take less time per token: 512 tokens x 2 heads of 128 50 us, 98 ns a token,
-// most of it the issue of a token's products and sums.
-cudaError_t launch_ssm_fwd_f32(const SsmParams &p, cudaStream_t s) {
+// 64 columns per CTA do the least work per token (B and C are read by fewer threads): 2048 tokens x 96 heads of 64 take 410 us.
+// Where that leaves the device mostly empty, 16 columns take half the time per token, 92 ns, most of it the issue of a token's products
+// and sums: 512 tokens x 2 heads of 128 50 us, 104 us with 64. A second CTA on an SM makes the two about 1.75 times as long.
+// Segments shorten the walk where CTAs are still few. The pass over the states takes half the time of a full one, and the second launch
+// and the folding about as long as 30 tokens and 2 per segment: 4096 tokens x 2 heads of 64 376 us in one piece and 43 in 16 segments,
+// 512 x 2 heads of 128 50 and 16 us, 128 x 2 heads of 128 15 and 9 us. At 256 CTAs of 2048 tokens two segments take 402 us and one 328.
+SsmRecPlan ssm_rec_plan(int n_seqs, long long T, int H, int P) {
+  SsmRecPlan l = {SSM_COLS, 1, 0};
+  if (n_seqs < 1) return l;
   int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  if ((long long)p.H * (p.P / 16) * p.n_seqs <= 2LL * sms) ssm_rec_kernel<16, 16><<<dim3(p.H * (p.P / 16), p.n_seqs), 288, 0, s>>>(p);
-  else ssm_rec_kernel<SSM_COLS, 8><<<dim3(p.H * (p.P / SSM_COLS), p.n_seqs), 288, 0, s>>>(p);
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+    (void)cudaGetLastError();
+    sms = 152;
+  }
+  if ((long long)H * (P / 16) * n_seqs <= 2LL * sms) l.cols = 16;
+  const long long ctas = (long long)H * (P / l.cols) * n_seqs;
+  const double each = (double)T / n_seqs;
+  auto walk = [&](long long n) -> double {   // how much longer n CTAs take than one
+    const double m = (double)((n + sms - 1) / sms);
+    return l.cols == 16 && m > 1 ? 0.87 * m : m;
+  };
+  double cost = each * walk(ctas);
+  for (int k = 2; k <= 16 && 16 * k <= each && (long long)n_seqs * k <= 65535; ++k) {
+    const double t = 1.5 * each / k * walk(ctas * k) + 30.0 + 2.0 * k;
+    if (t < cost) cost = t, l.nseg = k;
+  }
+  const size_t items = (size_t)(l.nseg - 1) * (size_t)ctas;
+  l.bytes = items * SSM_N * l.cols * sizeof(float) + (items * sizeof(float) + 255) / 256 * 256;
+  return l;
+}
+
+template <int W, int TB>
+cudaError_t launch_rec(const SsmParams &p, const SsmRecPlan &l, void *workspace, cudaStream_t s) {
+  const unsigned slices = (unsigned)(p.H * (p.P / W));
+  float *state = static_cast<float *>(workspace), *decay = state + (size_t)(l.nseg - 1) * p.n_seqs * slices * SSM_N * W;
+  if (l.nseg > 1) {
+    ssm_rec_kernel<W, TB, true><<<dim3(slices, p.n_seqs * (l.nseg - 1)), 288, 0, s>>>(p, l.nseg, state, decay);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  ssm_rec_kernel<W, TB, false><<<dim3(slices, p.n_seqs * l.nseg), 288, 0, s>>>(p, l.nseg, state, decay);
   return cudaGetLastError();
+}
+cudaError_t launch_ssm_fwd_f32(const SsmParams &p, const SsmRecPlan &l, void *workspace, cudaStream_t s) {
+  return l.cols == 16 ? launch_rec<16, 16>(p, l, workspace, s) : launch_rec<SSM_COLS, 8>(p, l, workspace, s);
 }
 
 cudaError_t launch_ssm_step(const SsmParams &p, bool f32, cudaStream_t s) {

@@ -358,3 +358,24 @@ def test_offsets_outside_the_tokens(kda, io):
     assert torch.equal(y, y1) and torch.equal(hT, hT1)
     y2, hT2 = call([0, 40, 20, 130])   # the second is empty, the third starts at 20
     assert torch.equal(hT2[1], s["h0"][1].cuda()) and torch.equal(hT2[0], hT[0])
+
+
+@pytest.mark.parametrize("lens,H,G,P", [([260], 1, 1, 64), ([900], 2, 1, 128), ([700, 0, 3, 650], 3, 1, 64), ([301, 300], 2, 2, 128), ([2048], 24, 1, 64)])
+def test_fp32_prompts_in_segments(kda, lens, H, G, P):
+    # few heads: the walk is cut, here into several segments, some of them empty
+    check(kda, lens, H, G, P, "f32", seed=31 + sum(lens))
+    check(kda, lens, H, G, P, "f32", seed=32 + sum(lens), h0=False, strength=0.01)   # what a segment holds reaches far into the next
+
+
+def test_fp32_segments_and_steps_agree(kda):
+    s = case([515], 2, 1, 64, "f32", 77, strength=0.02)
+    x, b, c = split(s["rows"].cuda(), 2, 1, 64)
+    kw = dict(d_skip=s["d_skip"].cuda(), dt_bias=s["dt_bias"].cuda())
+    y, hT = kda.ssm_fwd(x, s["dt"].cuda(), s["a"].cuda(), b, c, None, s["h0"].cuda(), **kw)
+    h, parts = s["h0"].cuda(), []
+    for t0 in range(0, 515, 30):   # pieces too short for a second segment
+        e = min(t0 + 30, 515)
+        yp, h = kda.ssm_fwd(x[t0:e], s["dt"][t0:e].cuda(), s["a"].cuda(), b[t0:e], c[t0:e], None, h, **kw)
+        parts.append(yp)
+    assert ref.rel(torch.cat(parts).cpu(), y.cpu().double()) <= 2 * TOL["f32"]
+    assert ref.rel(h.cpu(), hT.cpu().double()) <= 2 * TOL["f32"]
