@@ -615,22 +615,22 @@ def block_norm_bwd(u, w_post, stats, d_out, d_normed=None, *, gate=None, gate_ac
     gradients of its two results, None for zero. Returns a dict: du, dgate, dresidual in u's
     dtype and dw_post, dscale, dw_pre fp32 [d], None where the input was absent."""
     lib = library()
-    dev, di, f32 = u.device, u.get_device(), torch.float32
-    b = _lib.BlockNormBwdArgs()
-    b.fwd = _block_norm_args(u, w_post, gate, gate_act, residual, scale, w_pre, eps)
-    rows, d = b.fwd.rows, b.fwd.dim
-    for i, (name, w) in enumerate((("rstd_post", w_post), ("rstd_pre", w_pre))):
-        if w is not None:
-            setattr(b.fwd, name, _need(stats[i], name, f32, (rows,), di))
-    b.d_out, b.d_normed = _maybe(d_out, "d_out", u.dtype, u.shape, di), _maybe(d_normed, "d_normed", u.dtype, u.shape, di)
-    like = lambda t: None if t is None else torch.empty_like(u)
-    vec = lambda t: None if t is None else torch.empty(d, dtype=f32, device=dev)
-    g = {"du": torch.empty_like(u), "dgate": like(gate), "dresidual": like(residual), "dw_post": vec(w_post),
-         "dscale": vec(scale), "dw_pre": vec(w_pre)}
-    b.du, b.d_gate, b.d_residual = _ptr(g["du"]), _ptr(g["dgate"]), _ptr(g["dresidual"])
-    b.dw_post, b.dscale, b.dw_pre, b.dev_status = _ptr(g["dw_post"]), _ptr(g["dscale"]), _ptr(g["dw_pre"]), _ptr(dev_status)
+    di, f32, shape = u.get_device(), torch.float32, u.shape
+    n = _block_norm_args(u, w_post, gate, gate_act, residual, scale, w_pre, eps)
+    rows, d = n.rows, n.dim
+    if w_post is not None:
+        n.rstd_post = _need(stats[0], "rstd_post", f32, (rows,), di)
+    if w_pre is not None:
+        n.rstd_pre = _need(stats[1], "rstd_pre", f32, (rows,), di)
+    du = torch.empty_like(u)
+    dgate, dresidual = (None if t is None else torch.empty_like(u) for t in (gate, residual))
+    dw_post, dscale, dw_pre = (None if t is None else torch.empty_like(t) for t in (w_post, scale, w_pre))
+    b = _lib.BlockNormBwdArgs(
+        n, _maybe(d_out, "d_out", u.dtype, shape, di), _maybe(d_normed, "d_normed", u.dtype, shape, di), du.data_ptr(), _ptr(dgate),
+        _ptr(dresidual), _ptr(dw_post), _ptr(dscale), _ptr(dw_pre))
+    b.dev_status = _ptr(dev_status)
     ws_bytes = lib.kda_block_norm_bwd_workspace_size(C.byref(b))
-    ws = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
+    ws = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=u.device)
     b.workspace, b.workspace_bytes = ws.data_ptr(), ws_bytes
-    _lib.check(lib.kda_block_norm_bwd(C.byref(b), _stream_of(dev)))
-    return g
+    _lib.check(lib.kda_block_norm_bwd(C.byref(b), _stream_of(u.device)))
+    return {"du": du, "dgate": dgate, "dresidual": dresidual, "dw_post": dw_post, "dscale": dscale, "dw_pre": dw_pre}
