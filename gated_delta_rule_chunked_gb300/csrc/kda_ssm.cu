@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(288) ssm_rec_kernel(SsmParams p, int nseg, flo
 #pragma unroll
   for (int i = 0; i < R::R; ++i) S2[i][0] = two(S[i][0], S[i][1]), S2[i][1] = two(S[i][2], S[i][3]);
   if (!STATES && !scalars)
+#pragma unroll 4
     for (int k = 0; k < seg; ++k) {
       const size_t at = ((size_t)n * (nseg - 1) + k) * gridDim.x + blockIdx.x;
       const float dec = seg_decay[at];

@@ -150,8 +150,42 @@ __device__ __forceinline__ int nth_longest(const int *cu, int n_seqs, int r, int
   return scratch[MOST_SORTED];
 }
 
-// STATES: the segments' own state contributions and decays only.
-template <bool STATES>
+// w times half of a token's X as three bf16 tiles: 24 bits in truncated terms of 8, so the remainders are exact.
+__device__ __forceinline__ void weigh(const char *x, char *wx, int row, int half, float w) {
+  const f2 w2 = two(w, w), minus = two(-1.f, -1.f);
+#pragma unroll 1
+  for (int k = 4 * half; k < 4 * half + 4; ++k) {
+    const uint32_t at = row_chunk(row, k);
+    const uint4 v = *reinterpret_cast<const uint4 *>(x + at);
+    const uint32_t xw[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o0[4], o1[4], o2[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const f2 v0 = mul2(w2, unpack2(xw[e]));
+      const float2 a = of2(v0);
+      const f2 v1 = fma2(two(__uint_as_float(__float_as_uint(a.x) & 0xffff0000u), __uint_as_float(__float_as_uint(a.y) & 0xffff0000u)), minus, v0);
+      const float2 b = of2(v1);
+      const float2 r = of2(fma2(two(__uint_as_float(__float_as_uint(b.x) & 0xffff0000u), __uint_as_float(__float_as_uint(b.y) & 0xffff0000u)), minus, v1));
+      o0[e] = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x7632);
+      o1[e] = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x7632);
+      o2[e] = __byte_perm(__float_as_uint(r.x), __float_as_uint(r.y), 0x7632);
+    }
+    *reinterpret_cast<uint4 *>(wx + at) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+    *reinterpret_cast<uint4 *>(wx + 16384 + at) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+    *reinterpret_cast<uint4 *>(wx + 32768 + at) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+  }
+}
+// h of a token, and h a log2(e)
+__device__ __forceinline__ float step_of(float v, float bias, int softplus) {
+  const float b = v + bias;
+  return softplus ? log1pf(expf(-fabsf(b))) + fmaxf(b, 0.f) : b;
+}
+// 2^-200 is zero in fp32 already: a token that forgets more would only cost the differences of the sums after it their digits
+__device__ __forceinline__ float forgets(float h, float al) {
+  const float l = h * al;
+  return l < -200.f ? -200.f : l;
+}
+
 __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ SsmTcParams p) {
   using L = SsmSmem;
   extern __shared__ __align__(1024) char smem[];
@@ -161,9 +195,9 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
   }
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, row = tid & 127;
   const int role = warp >> 3, half = (warp >> 2) & 1, wq = warp & 3;   // eight warps per role, two per 32 rows
-  const int U = p.s.H * (p.s.P / SSM_COLS), nseg = p.nseg, runs = STATES ? nseg - 1 : nseg;
-  const int u = blockIdx.x % U, ns = blockIdx.x / U, seg = ns % runs;
-  const int n = p.sorted ? nth_longest(p.s.cu, p.s.n_seqs, ns / runs, reinterpret_cast<int *>(smem)) : ns / runs;
+  const int U = p.s.H * (p.s.P / SSM_COLS), nseg = p.nseg;
+  const int u = blockIdx.x % U, ns = blockIdx.x / U, seg = ns % nseg;
+  const int n = p.sorted ? nth_longest(p.s.cu, p.s.n_seqs, ns / nseg, reinterpret_cast<int *>(smem)) : ns / nseg;
   const int head = u / (p.s.P / SSM_COLS), col0 = (u % (p.s.P / SSM_COLS)) * SSM_COLS, group = head / (p.s.H / p.s.G);
   // token indices fit 32 bits (T < 2^31)
   // and offsets that are no sequence's are taken as an empty one
@@ -184,8 +218,8 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
       if (i >= MREADY0 && i <= MREADY3) count = 64 * (MREADY3 + 1 - i);
       if (i >= WXREADY0 && i <= WXREADY3) count = 64;
       if (i == SFULL) count = 32;
-      if (i == EMPTY0 || i == EMPTY1) count = STATES ? 1 : 2;
-      if (i == SEMPTY) count = STATES ? 512 : 768;
+      if (i == EMPTY0 || i == EMPTY1) count = 2;
+      if (i == SEMPTY) count = 768;
       mbar_init(&bar[i], count);
     }
     fence_mbar_init();
@@ -202,110 +236,108 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
   int c = 0;
 
   if (role == 0) {
-    if constexpr (!STATES) {
-      // ------------------------------------------------------------ M and Y
-      {
-        const uint32_t z[8] = {};
+    // ------------------------------------------------------------ M and Y
+    {
+      const uint32_t z[8] = {};
 #pragma unroll 1
-        for (int k = half; k < 8; k += 2) st8u(tl + T_M + 8 * k, z);   // blocks above the diagonal stay zero
-        tc::wait_st();
-      }
-      const float d = p.s.d_skip ? p.s.d_skip[head] : 0.f;
-      const f2 d2 = two(d, d);
-      f2 e2 = two(0.f, 0.f);
-      for (c = 0; c <= nch; ++c) {
-        if (c > 0) {   // the previous chunk's Y, while this chunk's G runs
-          const int k0 = c - 1, len = len_of(k0);
-          char *ys = smem + (k0 & 1) * L::STAGE + L::X;   // in the place of the chunk's X, which everything has read by then
-          ok = mbar_wait_quiet(&bar[YDONE], k0 & 1) && mbar_wait_quiet(&bar[XEMPTY0 + (k0 & 1)], (k0 >> 1) & 1);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          tc::fence_after();
-#pragma unroll 1
-          for (int k = 2 * half; k < 2 * half + 2; ++k) {
-            float v[16], u[16];
-            uint32_t o[8];
-            tc::ld16(tl + T_Y1 + 16 * k, v);
-            tc::ld16(tl + T_Y2 + 16 * k, u);
-            tc::wait_ld();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 xv = *reinterpret_cast<const uint4 *>(ys + row_chunk(row, 2 * k + h));
-              const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int j = 8 * h + 2 * i;
-                o[4 * h + i] = pack2(fma2(d2, unpack2(xw[i]), fma2(e2, two(u[j], u[j + 1]), two(v[j], v[j + 1]))));
-              }
-            }
-            *reinterpret_cast<uint4 *>(ys + row_chunk(row, 2 * k)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4 *>(ys + row_chunk(row, 2 * k + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-          }
-          tc::fence_before();
-          mbar_arrive(&bar[YFREE]);
-          fence_proxy_async();
-          mbar_arrive(&bar[YSTAGED0 + (k0 & 1)]);
-          if (len < Q && row < len) {   // a short last chunk: its box would reach into the next sequence
-            bf16 *out = static_cast<bf16 *>(p.s.y) + ((long long)(t_begin + k0 * Q + row) * p.s.H + head) * p.s.P + col0;
-#pragma unroll 1
-            for (int k = 4 * half; k < 4 * half + 4; ++k)
-              *reinterpret_cast<uint4 *>(out + 8 * k) = *reinterpret_cast<const uint4 *>(ys + row_chunk(row, k));
-          }
-        }
-        if (c == nch) break;
-        // M's columns are free: the products of the previous chunk were issued before this G
-        ok = mbar_wait_quiet(&bar[SFULL], c & 1) && mbar_wait_quiet(&bar[GDONE], c & 1);
+      for (int k = half; k < 8; k += 2) st8u(tl + T_M + 8 * k, z);   // blocks above the diagonal stay zero
+      tc::wait_st();
+    }
+    const float d = p.s.d_skip ? p.s.d_skip[head] : 0.f;
+    const f2 d2 = two(d, d);
+    f2 e2 = two(0.f, 0.f);
+    for (c = 0; c <= nch; ++c) {
+      if (c > 0) {   // the previous chunk's Y, while this chunk's G runs
+        const int k0 = c - 1, len = len_of(k0);
+        char *ys = smem + (k0 & 1) * L::STAGE + L::X;   // in the place of the chunk's X, which everything has read by then
+        ok = mbar_wait_quiet(&bar[YDONE], k0 & 1) && mbar_wait_quiet(&bar[XEMPTY0 + (k0 & 1)], (k0 >> 1) & 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc::fence_after();
-        const float ci = sc_c[row];
-        // M: row i, 16 columns at a time, every other block of 16 (the other half's warps take the rest). Left of the
-        // diagonal's 32 columns 2^(c_i - c_j) h_j = 2^(c_i - c_r) e_j with the last column r of j's 32,
-        // e_j = 2^(c_r - c_j) h_j (both exponents <= 0): no exponential per entry
 #pragma unroll 1
-        for (int jb = 0; jb < wq; ++jb) {
-          const int j0 = 32 * jb + 16 * half;
-          float g[16];
-          uint32_t m[8];
-          tc::ld16(tl + T_G + j0, g);
-          const float r = ex2(ci - sc_c[32 * jb + 31]);
-          const f2 r2 = two(r, r);
+        for (int k = 2 * half; k < 2 * half + 2; ++k) {
+          float v[16], u[16];
+          uint32_t o[8];
+          tc::ld16(tl + T_Y1 + 16 * k, v);
+          tc::ld16(tl + T_Y2 + 16 * k, u);
           tc::wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 e = *reinterpret_cast<const float4 *>(sc_e + j0 + j);
-            m[j / 2] = pack2(mul2(mul2(two(g[j], g[j + 1]), two(e.x, e.y)), r2));
-            m[j / 2 + 1] = pack2(mul2(mul2(two(g[j + 2], g[j + 3]), two(e.z, e.w)), r2));
-          }
-          st8u(tl + T_M + j0 / 2, m);
-          tc::wait_st();
-          tc::fence_before();
-          mbar_arrive(&bar[MREADY0 + jb]);
-        }
-        {
-          const int j0 = 32 * wq + 16 * half;
-          float g[16];
-          uint32_t m[8];
-          tc::ld16(tl + T_G + j0, g);
-          tc::wait_ld();
-          tc::fence_before();
-          mbar_arrive(&bar[GFREE]);
-          const uint32_t keep = ((2u << lane) - 1u) >> (16 * half);   // columns j <= i
-          const f2 c2 = two(ci, ci), minus = two(-1.f, -1.f);
+          for (int h = 0; h < 2; ++h) {
+            const uint4 xv = *reinterpret_cast<const uint4 *>(ys + row_chunk(row, 2 * k + h));
+            const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float2 cj = *reinterpret_cast<const float2 *>(sc_c + j0 + j), hj = *reinterpret_cast<const float2 *>(sc_h + j0 + j);
-            const float2 x = of2(fma2(two(cj.x, cj.y), minus, c2));
-            const float2 v = of2(mul2(mul2(two(ex2(x.x), ex2(x.y)), two(hj.x, hj.y)), two(g[j], g[j + 1])));
-            m[j / 2] = pack2(keep >> j & 1u ? v.x : 0.f, keep >> (j + 1) & 1u ? v.y : 0.f);
+            for (int i = 0; i < 4; ++i) {
+              const int j = 8 * h + 2 * i;
+              o[4 * h + i] = pack2(fma2(d2, unpack2(xw[i]), fma2(e2, two(u[j], u[j + 1]), two(v[j], v[j + 1]))));
+            }
           }
-          st8u(tl + T_M + j0 / 2, m);
-          tc::wait_st();
-          tc::fence_before();
-          mbar_arrive(&bar[MREADY0 + wq]);
+          *reinterpret_cast<uint4 *>(ys + row_chunk(row, 2 * k)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4 *>(ys + row_chunk(row, 2 * k + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
-        mbar_arrive(&bar[SEMPTY]);
-        const float ei = exp2f(ci);
-        e2 = two(ei, ei);
+        tc::fence_before();
+        mbar_arrive(&bar[YFREE]);
+        fence_proxy_async();
+        mbar_arrive(&bar[YSTAGED0 + (k0 & 1)]);
+        if (len < Q && row < len) {   // a short last chunk: its box would reach into the next sequence
+          bf16 *out = static_cast<bf16 *>(p.s.y) + ((long long)(t_begin + k0 * Q + row) * p.s.H + head) * p.s.P + col0;
+#pragma unroll 1
+          for (int k = 4 * half; k < 4 * half + 4; ++k)
+            *reinterpret_cast<uint4 *>(out + 8 * k) = *reinterpret_cast<const uint4 *>(ys + row_chunk(row, k));
+        }
       }
+      if (c == nch) break;
+      // M's columns are free: the products of the previous chunk were issued before this G
+      ok = mbar_wait_quiet(&bar[SFULL], c & 1) && mbar_wait_quiet(&bar[GDONE], c & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      tc::fence_after();
+      const float ci = sc_c[row];
+      // M: row i, 16 columns at a time, every other block of 16 (the other half's warps take the rest). Left of the
+      // diagonal's 32 columns 2^(c_i - c_j) h_j = 2^(c_i - c_r) e_j with the last column r of j's 32,
+      // e_j = 2^(c_r - c_j) h_j (both exponents <= 0): no exponential per entry
+#pragma unroll 1
+      for (int jb = 0; jb < wq; ++jb) {
+        const int j0 = 32 * jb + 16 * half;
+        float g[16];
+        uint32_t m[8];
+        tc::ld16(tl + T_G + j0, g);
+        const float r = ex2(ci - sc_c[32 * jb + 31]);
+        const f2 r2 = two(r, r);
+        tc::wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 e = *reinterpret_cast<const float4 *>(sc_e + j0 + j);
+          m[j / 2] = pack2(mul2(mul2(two(g[j], g[j + 1]), two(e.x, e.y)), r2));
+          m[j / 2 + 1] = pack2(mul2(mul2(two(g[j + 2], g[j + 3]), two(e.z, e.w)), r2));
+        }
+        st8u(tl + T_M + j0 / 2, m);
+        tc::wait_st();
+        tc::fence_before();
+        mbar_arrive(&bar[MREADY0 + jb]);
+      }
+      {
+        const int j0 = 32 * wq + 16 * half;
+        float g[16];
+        uint32_t m[8];
+        tc::ld16(tl + T_G + j0, g);
+        tc::wait_ld();
+        tc::fence_before();
+        mbar_arrive(&bar[GFREE]);
+        const uint32_t keep = ((2u << lane) - 1u) >> (16 * half);   // columns j <= i
+        const f2 c2 = two(ci, ci), minus = two(-1.f, -1.f);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float2 cj = *reinterpret_cast<const float2 *>(sc_c + j0 + j), hj = *reinterpret_cast<const float2 *>(sc_h + j0 + j);
+          const float2 x = of2(fma2(two(cj.x, cj.y), minus, c2));
+          const float2 v = of2(mul2(mul2(two(ex2(x.x), ex2(x.y)), two(hj.x, hj.y)), two(g[j], g[j + 1])));
+          m[j / 2] = pack2(keep >> j & 1u ? v.x : 0.f, keep >> (j + 1) & 1u ? v.y : 0.f);
+        }
+        st8u(tl + T_M + j0 / 2, m);
+        tc::wait_st();
+        tc::fence_before();
+        mbar_arrive(&bar[MREADY0 + wq]);
+      }
+      mbar_arrive(&bar[SEMPTY]);
+      const float ei = exp2f(ci);
+      e2 = two(ei, ei);
     }
   } else if (role == 1) {
     // -------------------------------------------------------------- w o X
@@ -331,29 +363,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
       }
       if (c > 0) ok = mbar_wait_quiet(&bar[DSPART0 + wq], (c - 1) & 1);   // the previous terms of these tokens are read
       if (!ok) break;
-      const f2 w2 = two(w, w), minus = two(-1.f, -1.f);
-#pragma unroll 1
-      for (int k = 4 * half; k < 4 * half + 4; ++k) {
-        const uint32_t at = row_chunk(row, k);
-        const uint4 v = *reinterpret_cast<const uint4 *>(st + L::X + at);
-        const uint32_t xw[4] = {v.x, v.y, v.z, v.w};
-        uint32_t o0[4], o1[4], o2[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // 24 bits in three truncated terms of 8: the remainders are exact
-          const f2 v0 = mul2(w2, unpack2(xw[e]));
-          const float2 a = of2(v0);
-          const f2 v1 = fma2(two(__uint_as_float(__float_as_uint(a.x) & 0xffff0000u), __uint_as_float(__float_as_uint(a.y) & 0xffff0000u)), minus, v0);
-          const float2 b = of2(v1);
-          const float2 r = of2(fma2(two(__uint_as_float(__float_as_uint(b.x) & 0xffff0000u), __uint_as_float(__float_as_uint(b.y) & 0xffff0000u)), minus, v1));
-          o0[e] = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x7632);
-          o1[e] = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x7632);
-          o2[e] = __byte_perm(__float_as_uint(r.x), __float_as_uint(r.y), 0x7632);
-        }
-        *reinterpret_cast<uint4 *>(smem + L::WX + at) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-        *reinterpret_cast<uint4 *>(smem + L::WX + 16384 + at) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-        *reinterpret_cast<uint4 *>(smem + L::WX + 32768 + at) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
-      }
+      weigh(st + L::X, smem + L::WX, row, half, w);
       fence_proxy_async();
       mbar_arrive(&bar[WXREADY0 + wq]);
       mbar_arrive(&bar[XEMPTY0 + (c & 1)]);
@@ -362,30 +372,14 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
   } else if (role == 2) {
     // -------------------------------------------------------------- the state: row n of [128][64], 32 columns
     f2 S[16];   // pairs of columns
-    const size_t plane = (size_t)SSM_N * SSM_COLS;
-    const size_t soff = (((size_t)n * p.s.H + head) * SSM_N + row) * p.s.P + col0 + 32 * half;
-    if (!STATES && p.s.h0) {
+    auto place = [&]() { return (((size_t)n * p.s.H + head) * SSM_N + row) * p.s.P + col0 + 32 * half; };   // of the row in h0 and hT
+    const float *from = p.s.h0 ? p.s.h0 + place() : nullptr;
+    if (seg > 0) from = p.seg_state + ((((size_t)n * (nseg - 1) + seg - 1) * U + u) * SSM_N + row) * SSM_COLS + 32 * half;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 v = *reinterpret_cast<const float4 *>(p.s.h0 + soff + 4 * i);
-        S[2 * i] = two(v.x, v.y), S[2 * i + 1] = two(v.z, v.w);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) S[i] = two(0.f, 0.f);
+    for (int i = 0; i < 8; ++i) {
+      const float4 v = from ? *reinterpret_cast<const float4 *>(from + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      S[2 * i] = two(v.x, v.y), S[2 * i + 1] = two(v.z, v.w);
     }
-    if (!STATES)
-      for (int k = 0; k < seg; ++k) {   // the segments before this one
-        const size_t at = ((size_t)n * (nseg - 1) + k) * U + u;
-        const float dec = p.seg_decay[at];
-        const float *e = p.seg_state + at * plane + (size_t)row * SSM_COLS + 32 * half;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 v = __ldcg(reinterpret_cast<const float4 *>(e + 4 * i));
-          S[2 * i] = fma2(S[2 * i], two(dec, dec), two(v.x, v.y));
-          S[2 * i + 1] = fma2(S[2 * i + 1], two(dec, dec), two(v.z, v.w));
-        }
-      }
     auto put = [&]() {   // the operand tile
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -394,8 +388,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
       fence_proxy_async();
       mbar_arrive(&bar[SREADY]);
     };
-    if (!STATES) put();
-    float log_dec = 0.f;
+    put();
     for (c = 0; c < nch; ++c) {
       ok = mbar_wait_quiet(&bar[SFULL], c & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -403,7 +396,6 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
       mbar_arrive(&bar[SEMPTY]);
       const float dec = exp2f(last);
       const f2 dec2 = two(dec, dec);
-      log_dec += last;
       ok = mbar_wait_quiet(&bar[DSDONE], c & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::fence_after();
@@ -420,28 +412,18 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
       }
       tc::fence_before();
       mbar_arrive(&bar[DSFREE]);
-      if (!STATES && c + 1 < nch) {
+      if (c + 1 < nch) {
         ok = mbar_wait_quiet(&bar[YDONE], c & 1);   // C S has read the previous operand
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         put();
       }
     }
-    if (ok) {
-      float *dst = nullptr;
-      if (STATES) {
-        const size_t at = ((size_t)n * (nseg - 1) + seg) * U + u;
-        dst = p.seg_state + at * plane + (size_t)row * SSM_COLS + 32 * half;
-        if (row == 0 && half == 0) p.seg_decay[at] = exp2f(log_dec);
-      } else if (p.s.hT && seg == nseg - 1) {
-        dst = p.s.hT + soff;
-      }
-      if (dst)
+    if (ok && p.s.hT && seg == nseg - 1)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 a = of2(S[2 * i]), b = of2(S[2 * i + 1]);
-          *reinterpret_cast<float4 *>(dst + 4 * i) = make_float4(a.x, a.y, b.x, b.y);
-        }
-    }
+      for (int i = 0; i < 8; ++i) {
+        const float2 a = of2(S[2 * i]), b = of2(S[2 * i + 1]);
+        *reinterpret_cast<float4 *>(p.s.hT + place() + 4 * i) = make_float4(a.x, a.y, b.x, b.y);
+      }
   } else if (warp == 24) {
     // -------------------------------------------------------------- scalars: lane l has tokens 4 l .. 4 l + 3
     const float al = p.s.a[head] * LOG2E, bias = p.s.dt_bias ? p.s.dt_bias[head] : 0.f;
@@ -461,18 +443,13 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
       if (c + 1 < nch) fetch(c + 1, v);
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {   // one body for the four: the values rotate
-        const float b = h[0] + bias;
-        const float x = p.s.softplus ? log1pf(expf(-fabsf(b))) + fmaxf(b, 0.f) : b;
+        const float x = step_of(h[0], bias, p.s.softplus);
         h[0] = h[1], h[1] = h[2], h[2] = h[3];
         h[3] = 4 * lane + i < len ? x : 0.f;
       }
       float la[4], pre[4], suf[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        la[i] = h[i] * al;
-        // 2^-200 is zero in fp32 already: a token that forgets more would only cost the differences of the sums after it their digits
-        la[i] = la[i] < -200.f ? -200.f : la[i];
-      }
+      for (int i = 0; i < 4; ++i) la[i] = forgets(h[i], al);
       pre[0] = la[0];
 #pragma unroll
       for (int i = 1; i < 4; ++i) pre[i] = pre[i - 1] + la[i];
@@ -520,23 +497,23 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
         return true;
       };
 #pragma unroll 1
-      for (c = 0; c < nch + (STATES ? 0 : 2); ++c) {
+      for (c = 0; c < nch + 2; ++c) {
         char *st = smem + (c & 1) * L::STAGE;
         const int t = t_begin + c * Q;
         if (c < nch) {   // B and C first: they are free before Y has left from X's place
           if (c >= 2) ok = mbar_wait_quiet(&bar[EMPTY0 + (c & 1)], ((c >> 1) - 1) & 1);
           if (!ok) break;
           uint64_t *b = &bar[FULL0 + (c & 1)];
-          mbar_expect_tx(b, STATES ? 32768 : 65536);
-          for (int k = 0; k < (STATES ? 2 : 4); ++k)   // B's two halves, C's two
+          mbar_expect_tx(b, 65536);
+          for (int k = 0; k < 4; ++k)   // B's two halves, C's two
             tc::tma_load_2d(st + (k < 2 ? L::B : L::C) + 16384 * (k & 1), k < 2 ? &p.tm_b : &p.tm_c, group * SSM_N + 64 * (k & 1), t, b);
           issued = c + 1;
           if (c + 1 < nch) {   // the next chunk's boxes into L2
-            for (int k = 0; k < (STATES ? 2 : 4); ++k) prefetch_2d(k < 2 ? &p.tm_b : &p.tm_c, group * SSM_N + 64 * (k & 1), t + Q);
+            for (int k = 0; k < 4; ++k) prefetch_2d(k < 2 ? &p.tm_b : &p.tm_c, group * SSM_N + 64 * (k & 1), t + Q);
             prefetch_2d(&p.tm_x, head * p.s.P + col0, t + Q);
           }
         }
-        if (c >= 2) ok = STATES ? mbar_wait_quiet(&bar[XEMPTY0 + (c & 1)], ((c >> 1) - 1) & 1) : store(c - 2);
+        if (c >= 2) ok = store(c - 2);
         if (!ok) break;
         if (c < nch) {
           mbar_expect_tx(&bar[XFULL0 + (c & 1)], 16384);
@@ -549,52 +526,50 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
       for (int k = issued > 2 ? issued - 2 : 0; k < issued; ++k) mbar_wait_quiet(&bar[FULL0 + (k & 1)], (k >> 1) & 1);
 #pragma unroll 1
       for (int k = xissued > 2 ? xissued - 2 : 0; k < xissued; ++k) mbar_wait_quiet(&bar[XFULL0 + (k & 1)], (k >> 1) & 1);
-      if (!STATES) bulk_wait_all();
+      bulk_wait_all();
     }
     __syncwarp();
   } else if (warp == 25) {
-    if constexpr (!STATES) {
-      // ------------------------------------------------------------ G, C S, M X
-      const uint32_t leader = elect();
-      const uint32_t d_s = dlo(smem_u32(smem + L::S), 8192);
-      auto all = [&](bool w) { return (bool)__all_sync(0xffffffffu, w); };
+    // ------------------------------------------------------------ G, C S, M X
+    const uint32_t leader = elect();
+    const uint32_t d_s = dlo(smem_u32(smem + L::S), 8192);
+    auto all = [&](bool w) { return (bool)__all_sync(0xffffffffu, w); };
 #pragma unroll 1
-      for (c = 0; c < nch; ++c) {
-        const uint32_t st = smem_u32(smem + (c & 1) * L::STAGE);
-        const uint32_t d_c = dlo(st + L::C, 16), d_b = dlo(st + L::B, 16), d_x = dlo(st + L::X, 8192);
-        ok = mbar_wait_quiet(&bar[FULL0 + (c & 1)], (c >> 1) & 1) && (c == 0 || mbar_wait_quiet(&bar[GFREE], (c - 1) & 1)) && (len_of(c) == Q || mbar_wait_quiet(&bar[TAIL], 0));
-        if (!(ok = all(ok))) break;
-        tc::fence_after();
+    for (c = 0; c < nch; ++c) {
+      const uint32_t st = smem_u32(smem + (c & 1) * L::STAGE);
+      const uint32_t d_c = dlo(st + L::C, 16), d_b = dlo(st + L::B, 16), d_x = dlo(st + L::X, 8192);
+      ok = mbar_wait_quiet(&bar[FULL0 + (c & 1)], (c >> 1) & 1) && (c == 0 || mbar_wait_quiet(&bar[GFREE], (c - 1) & 1)) && (len_of(c) == Q || mbar_wait_quiet(&bar[TAIL], 0));
+      if (!(ok = all(ok))) break;
+      tc::fence_after();
 #pragma unroll
-        for (uint32_t ks = 0; ks < 8; ++ks) {
-          const uint32_t o = (ks >> 2) * (16384 >> 4) + (ks & 3) * 2;
-          mma_ss(leader, tmem + T_G, desc(d_c + o), desc(d_b + o), tc::idesc_bf16(128, 128), ks > 0);
-        }
-        commit(leader, &bar[GDONE]);
-        ok = mbar_wait_quiet(&bar[SREADY], c & 1) && (c == 0 || mbar_wait_quiet(&bar[YFREE], (c - 1) & 1));
-        if (!(ok = all(ok))) break;
-        tc::fence_after();
-#pragma unroll
-        for (uint32_t ks = 0; ks < 8; ++ks)
-          mma_ss(leader, tmem + T_Y2, desc(d_c + (ks >> 2) * (16384 >> 4) + (ks & 3) * 2), desc(d_s + ks * (2048 >> 4)),
-                 tc::idesc_bf16_mn(128, 64, false, true), ks > 0);
-        commit(leader, &bar[EMPTY0 + (c & 1)]);
-        ok = mbar_wait_quiet(&bar[XFULL0 + (c & 1)], (c >> 1) & 1);
-#pragma unroll
-        for (uint32_t k = 0; k < 4; ++k) {   // as M's column blocks become ready
-          ok = ok && all(mbar_wait_quiet(&bar[MREADY0 + k], c & 1));
-          if (ok) {
-            tc::fence_after();
-            mma_ts(leader, tmem + T_Y1, tmem + T_M + 16 * k, desc(d_x + k * (4096 >> 4)), tc::idesc_bf16_mn(128, 64, false, true), k > 0);
-            mma_ts(leader, tmem + T_Y1, tmem + T_M + 16 * k + 8, desc(d_x + k * (4096 >> 4) + (2048 >> 4)), tc::idesc_bf16_mn(128, 64, false, true), 1);
-          }
-        }
-        if (!ok) break;
-        commit(leader, &bar[YDONE]);
+      for (uint32_t ks = 0; ks < 8; ++ks) {
+        const uint32_t o = (ks >> 2) * (16384 >> 4) + (ks & 3) * 2;
+        mma_ss(leader, tmem + T_G, desc(d_c + o), desc(d_b + o), tc::idesc_bf16(128, 128), ks > 0);
       }
-      commit(leader, &bar[DRAIN0]);   // nothing of this thread runs on once the CTA leaves
-      ok &= mbar_wait_quiet(&bar[DRAIN0], 0);
+      commit(leader, &bar[GDONE]);
+      ok = mbar_wait_quiet(&bar[SREADY], c & 1) && (c == 0 || mbar_wait_quiet(&bar[YFREE], (c - 1) & 1));
+      if (!(ok = all(ok))) break;
+      tc::fence_after();
+#pragma unroll
+      for (uint32_t ks = 0; ks < 8; ++ks)
+        mma_ss(leader, tmem + T_Y2, desc(d_c + (ks >> 2) * (16384 >> 4) + (ks & 3) * 2), desc(d_s + ks * (2048 >> 4)),
+               tc::idesc_bf16_mn(128, 64, false, true), ks > 0);
+      commit(leader, &bar[EMPTY0 + (c & 1)]);
+      ok = mbar_wait_quiet(&bar[XFULL0 + (c & 1)], (c >> 1) & 1);
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k) {   // as M's column blocks become ready
+        ok = ok && all(mbar_wait_quiet(&bar[MREADY0 + k], c & 1));
+        if (ok) {
+          tc::fence_after();
+          mma_ts(leader, tmem + T_Y1, tmem + T_M + 16 * k, desc(d_x + k * (4096 >> 4)), tc::idesc_bf16_mn(128, 64, false, true), k > 0);
+          mma_ts(leader, tmem + T_Y1, tmem + T_M + 16 * k + 8, desc(d_x + k * (4096 >> 4) + (2048 >> 4)), tc::idesc_bf16_mn(128, 64, false, true), 1);
+        }
+      }
+      if (!ok) break;
+      commit(leader, &bar[YDONE]);
     }
+    commit(leader, &bar[DRAIN0]);   // nothing of this thread runs on once the CTA leaves
+    ok &= mbar_wait_quiet(&bar[DRAIN0], 0);
   } else {
     // -------------------------------------------------------------- B^T (w o X)
     const uint32_t leader = elect();
@@ -628,6 +603,216 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
   if (warp == 25) tc::dealloc(tmem, 512);
 }
 
+// What a segment of whole chunks adds to the state, sum_j w_j B_j x_j^T, and its decay. With w counted to the segment's end instead of
+// the chunk's, the chunks' products only have to be added up. The chunks go from the last to the first, so that a chunk's weights need
+// only the sum of h a over the chunks already taken. Two sets of eight warps take every other chunk: w o X into the set's tiles, and the
+// products of its previous chunk out of its half of tensor memory into fp32 registers (left there to add up over a segment they would
+// be truncated at every step: the state was off by 1.4e-5 of its largest value after 85 chunks, now by 7e-7). Warp 16 has the scalars,
+// warp 17 the products, warp 18 the loads. X has a third stage, so that it is there when a set's tiles have been read; B is not needed
+// before w o X is formed. About 0.9 us a chunk where the scan itself takes 1.9.
+struct StSmem {
+  static constexpr int B = 0, X = 2 * 32768;
+  static constexpr int WX = X + 3 * 16384;   // three terms per set
+  static constexpr int SC = WX + 2 * 49152;  // fp32 w of the set's tokens
+  static constexpr int BAR = SC + 2 * Q * 4;
+  static constexpr int TSLOT = BAR + 20 * 8;
+  static constexpr int BYTES = TSLOT + 16;
+};
+// two of each, by set, but three of X's and one for the end
+enum StBar { ST_B, ST_WX = 2, ST_READ = 4, ST_S = 6, ST_SFREE = 8, ST_X = 10, ST_XFREE = 13, ST_END = 16, ST_NBAR };
+static_assert(ST_NBAR <= 20 && StSmem::BYTES <= 232448, "places");
+
+__global__ void __launch_bounds__(608, 1) ssm_states_kernel(const __grid_constant__ SsmTcParams p) {
+  using L = StSmem;
+  extern __shared__ __align__(1024) char smem[];
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) report(p.s.status, 3 /* KDA_ERR_CUDA */);
+    return;
+  }
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, row = tid & 127;
+  const int U = p.s.H * (p.s.P / SSM_COLS), nseg = p.nseg;
+  const int u = blockIdx.x % U, ns = blockIdx.x / U, seg = ns % (nseg - 1), n = ns / (nseg - 1);
+  const int head = u / (p.s.P / SSM_COLS), col0 = (u % (p.s.P / SSM_COLS)) * SSM_COLS, group = head / (p.s.H / p.s.G);
+  const int each = (int)(p.s.T / p.s.n_seqs), seq0 = max(p.s.cu ? p.s.cu[n] : each * n, 0);
+  const int seq1 = max(min(p.s.cu ? p.s.cu[n + 1] : each * (n + 1), (int)p.s.T), seq0);
+  const int all = (int)(((unsigned)(seq1 - seq0) + Q - 1) / Q);
+  const int first = (int)((long long)all * seg / nseg), nch = (int)((long long)all * (seg + 1) / nseg) - first;
+  auto token = [&](int i) { return seq0 + (first + nch - 1 - i) * Q; };   // of the i-th chunk taken: a whole one, the last segment is not run
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + L::BAR);
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + L::TSLOT);
+  float *sc_w = reinterpret_cast<float *>(smem + L::SC);
+  if (tid == 0) {
+    for (int i = 0; i < ST_NBAR; ++i) mbar_init(&bar[i], i / 2 == ST_WX / 2 || i / 2 == ST_SFREE / 2 || (i >= ST_XFREE && i < ST_END) ? 256 : i / 2 == ST_S / 2 ? 32 : 1);
+    fence_mbar_init();
+  }
+  if (warp == 17) tc::alloc(tslot, 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tslot;
+  const size_t at = ((size_t)n * (nseg - 1) + seg) * U + u;
+  bool ok = true;
+  if (warp < 16) {
+    const int set = warp >> 3, half = (warp >> 2) & 1;
+    const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 192 * set + 32 * half;
+    f2 S[16];   // 32 columns of a row
+#pragma unroll
+    for (int i = 0; i < 16; ++i) S[i] = two(0.f, 0.f);
+    auto take = [&](int i) {   // chunk i's products
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_quiet(&bar[ST_READ + set], (i >> 1) & 1));
+      if (!ok) return;
+      tc::fence_after();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float d0[8], d1[8], d2[8];
+        ld8(from + 8 * k, d0);
+        ld8(from + 64 + 8 * k, d1);
+        ld8(from + 128 + 8 * k, d2);
+        tc::wait_ld();
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          S[4 * k + e] = add2(S[4 * k + e], add2(two(d0[2 * e], d0[2 * e + 1]), add2(two(d1[2 * e], d1[2 * e + 1]), two(d2[2 * e], d2[2 * e + 1]))));
+      }
+      tc::fence_before();
+    };
+    int xs = set, xphase = 0, i = set;   // i % 3, i / 3 & 1
+    for (; i < nch; i += 2) {
+      if (i >= 2) take(i - 2);
+      ok = ok && mbar_wait_quiet(&bar[ST_X + xs], xphase) && mbar_wait_quiet(&bar[ST_S + set], (i >> 1) & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const float w = sc_w[set * Q + row];
+      mbar_arrive(&bar[ST_SFREE + set]);
+      weigh(smem + L::X + 16384 * xs, smem + L::WX + 49152 * set, row, half, w);
+      fence_proxy_async();
+      mbar_arrive(&bar[ST_WX + set]);
+      mbar_arrive(&bar[ST_XFREE + xs]);
+      xs += 2;
+      if (xs >= 3) xs -= 3, xphase ^= 1;
+    }
+    if (i >= 2) take(i - 2);
+    // the second set's sums join the first's; every product and load is done with this part of shared memory once both have taken theirs
+    char *meet = smem + L::WX + row * 256;
+    asm volatile("bar.sync 1, 512;\n" ::: "memory");
+    if (set == 1)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 a = of2(S[2 * k]), b = of2(S[2 * k + 1]);
+        *reinterpret_cast<float4 *>(meet + (((8 * half + k) ^ (row & 15)) << 4)) = make_float4(a.x, a.y, b.x, b.y);
+      }
+    asm volatile("bar.sync 1, 512;\n" ::: "memory");
+    if (set == 0) {
+      float *dst = p.seg_state + at * SSM_N * SSM_COLS + (size_t)row * SSM_COLS + 32 * half;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float4 o = *reinterpret_cast<const float4 *>(meet + (((8 * half + k) ^ (row & 15)) << 4));
+        const float2 a = of2(S[2 * k]), b = of2(S[2 * k + 1]);
+        *reinterpret_cast<float4 *>(dst + 4 * k) = make_float4(a.x + o.x, a.y + o.y, b.x + o.z, b.y + o.w);
+      }
+    }
+  } else if (warp == 16) {   // lane l has tokens 4 l .. 4 l + 3
+    const float al = p.s.a[head] * LOG2E, bias = p.s.dt_bias ? p.s.dt_bias[head] : 0.f;
+    auto fetch = [&](int i, float (&v)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = p.s.dt[(long long)(token(i) + 4 * lane + k) * p.s.H + head];
+    };
+    float v[4], later = 0.f;   // sum of h a over the chunks taken
+    if (nch > 0) fetch(0, v);
+    for (int i = 0; i < nch; ++i) {
+      float h[4], w[4], suf[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[k] = step_of(v[k], bias, p.s.softplus);
+      if (i + 1 < nch) fetch(i + 1, v);
+      suf[3] = 0.f;
+#pragma unroll
+      for (int k = 2; k >= 0; --k) suf[k] = suf[k + 1] + forgets(h[k + 1], al);
+      float above = suf[0] + forgets(h[0], al);
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const float z = __shfl_down_sync(0xffffffffu, above, o);
+        if (lane + o < 32) above += z;
+      }
+      const float right = __shfl_down_sync(0xffffffffu, above, 1), ab = (lane < 31 ? right : 0.f) + later;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = h[k] * exp2f(suf[k] + ab);
+      later += __shfl_sync(0xffffffffu, above, 0);
+      if (i >= 2) ok = mbar_wait_quiet(&bar[ST_SFREE + (i & 1)], ((i >> 1) - 1) & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      *reinterpret_cast<float4 *>(sc_w + (i & 1) * Q + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
+      mbar_arrive(&bar[ST_S + (i & 1)]);
+    }
+    if (lane == 0) p.seg_decay[at] = exp2f(later);
+  } else if (warp == 17) {
+    const uint32_t leader = elect();
+#pragma unroll 1
+    for (int i = 0; i < nch; ++i) {
+      const uint32_t d_b = dlo(smem_u32(smem + L::B + (i & 1) * 32768), 16384), d_w = dlo(smem_u32(smem + L::WX + (i & 1) * 49152), 16384);
+      ok = mbar_wait_quiet(&bar[ST_B + (i & 1)], (i >> 1) & 1) && mbar_wait_quiet(&bar[ST_WX + (i & 1)], (i >> 1) & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      tc::fence_after();
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k)
+        mma_ss(leader, tmem + 192 * (i & 1), desc(d_b + k * (2048 >> 4)), desc(d_w + k * (2048 >> 4)), tc::idesc_bf16_mn(128, 192, true, true), k > 0);
+      commit(leader, &bar[ST_READ + (i & 1)]);
+    }
+    commit(leader, &bar[ST_END]);
+    ok &= mbar_wait_quiet(&bar[ST_END], 0);
+  } else if (lane == 0) {
+    int issued = 0, xissued = 0, xs = 0, xphase = 0;
+    auto load_x = [&]() {   // of the next chunk that has none
+      if (xissued >= 3 && !mbar_wait_quiet(&bar[ST_XFREE + xs], xphase ^ 1)) return false;
+      mbar_expect_tx(&bar[ST_X + xs], 16384);
+      tc::tma_load_2d(smem + L::X + 16384 * xs, &p.tm_x, head * p.s.P + col0, token(xissued), &bar[ST_X + xs]);
+      ++xissued;
+      if (++xs == 3) xs = 0, xphase ^= 1;
+      return true;
+    };
+    if (nch > 0) ok = load_x();
+    for (int i = 0; i < nch && ok; ++i) {
+      if (xissued < nch) ok = load_x();
+      if (ok && i >= 2) ok = mbar_wait_quiet(&bar[ST_READ + (i & 1)], ((i >> 1) - 1) & 1);
+      if (!ok) break;
+      mbar_expect_tx(&bar[ST_B + (i & 1)], 32768);
+      for (int k = 0; k < 2; ++k) tc::tma_load_2d(smem + L::B + 32768 * (i & 1) + 16384 * k, &p.tm_b, group * SSM_N + 64 * k, token(i), &bar[ST_B + (i & 1)]);
+      issued = i + 1;
+      if (i + 2 < nch) {
+        prefetch_2d(&p.tm_x, head * p.s.P + col0, token(i + 2));
+        for (int k = 0; k < 2; ++k) prefetch_2d(&p.tm_b, group * SSM_N + 64 * k, token(i + 2));
+      }
+    }
+    // everything has landed before the CTA leaves, also after a timeout
+    for (int i = issued > 2 ? issued - 2 : 0; i < issued; ++i) ok &= mbar_wait_quiet(&bar[ST_B + (i & 1)], (i >> 1) & 1);
+    for (int i = xissued > 3 ? xissued - 3 : 0; i < xissued; ++i) ok &= mbar_wait_quiet(&bar[ST_X + i % 3], (i / 3) & 1);
+  }
+  if (!ok) report(p.s.status, ERR_TIMEOUT);
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 17) tc::dealloc(tmem, 512);
+}
+
+// From what the segments add and their decays to the states that the segments after them start from, in place. Grid: (units of all
+// sequences, eighths of a state); a thread has four columns of a row, all segments' on their way at once.
+constexpr int MOST_SEGS = 16;
+__global__ void __launch_bounds__(256) ssm_fold_kernel(SsmTcParams p) {
+  const int U = p.s.H * (p.s.P / SSM_COLS), u = blockIdx.x % U, n = blockIdx.x / U, m = p.nseg - 1;
+  const int head = u / (p.s.P / SSM_COLS), col0 = (u % (p.s.P / SSM_COLS)) * SSM_COLS, e = blockIdx.y * 256 + threadIdx.x;
+  float4 v[MOST_SEGS - 1];
+  float dec[MOST_SEGS - 1];
+  auto place = [&](int k) { return reinterpret_cast<float4 *>(p.seg_state + (((size_t)n * m + k) * U + u) * SSM_N * SSM_COLS) + e; };
+#pragma unroll
+  for (int k = 0; k < MOST_SEGS - 1; ++k)
+    if (k < m) v[k] = *place(k), dec[k] = p.seg_decay[((size_t)n * m + k) * U + u];
+  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.s.h0) S = *reinterpret_cast<const float4 *>(p.s.h0 + (((size_t)n * p.s.H + head) * SSM_N + e / 16) * p.s.P + col0 + e % 16 * 4);
+#pragma unroll
+  for (int k = 0; k < MOST_SEGS - 1; ++k)
+    if (k < m) {
+      S.x = fmaf(S.x, dec[k], v[k].x), S.y = fmaf(S.y, dec[k], v[k].y), S.z = fmaf(S.z, dec[k], v[k].z), S.w = fmaf(S.w, dec[k], v[k].w);
+      *place(k) = S;
+    }
+}
+
 bool map_rows(EncodeTiledFn fn, CUtensorMap *m, const void *base, long long rows, long long width, long long ld) {
   const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
@@ -637,11 +822,10 @@ bool map_rows(EncodeTiledFn fn, CUtensorMap *m, const void *base, long long rows
 }
 }  // namespace
 
-// Segments per sequence: the count that takes the fewest chunk times (about 2 us each). Without segments
-// every wave of CTAs walks whole sequences; with k, a wave walks 1/k of them, in two passes of which the
-// first costs about as much as the second (at 96 heads of one 32768-token prompt, 0.52 ms without and
-// 0.76 ms with 11 segments; at 24 units of 4096 tokens, 0.11 and 0.07 ms), plus the second launch and the
-// folding.
+// Segments per sequence: the count that takes the fewest chunk times (about 1.9 us each). Every wave of CTAs walks a k-th of a sequence;
+// the states' pass takes half of a full chunk's time per chunk, a wave's start about 2.5 chunk times, the two further launches 3 and
+// each segment half of one. 32768 tokens x 24 units (heads x head_dim / 64): 477 us in one piece, 138 in 6 segments; x 40 units 480 us,
+// 257 in 3, 247 in 11; x 96 units, which keep 96 SMs busy, 483 us and at best 518, in 3. 4096 tokens x 24 units: 67 and 34 us.
 int ssm_segments(int n_seqs, long long T, int units) {
   if (n_seqs < 1 || T < 1) return 1;
   int dev = 0, sms = 0;
@@ -649,11 +833,13 @@ int ssm_segments(int n_seqs, long long T, int units) {
     (void)cudaGetLastError();
     sms = 152;
   }
-  const double chunks = (double)T / n_seqs / Q, pairs = (double)n_seqs * units;
+  const double chunks = (double)T / n_seqs / Q;
+  auto waves = [&](long long k) { return (double)(((long long)n_seqs * units * k + sms - 1) / sms); };
   int best = 1;
-  double cost = chunks * (double)(long long)((pairs + sms - 1) / sms);
-  for (int k = 2; k <= 16 && k * 2 <= chunks; ++k) {
-    const double t = 2.0 * chunks / k * (double)(long long)((pairs * k + sms - 1) / sms) + 4.0 + 0.5 * k;
+  double cost = (chunks + 2.5) * waves(1) + 2.0;
+  for (int k = 2; k <= MOST_SEGS && k * 2 <= chunks; ++k) {
+    const double full = waves(k), states = waves(k - 1);
+    const double t = chunks / k * (full + 0.5 * states) + 2.5 * (full + states) + 5.0 + 0.5 * k;
     if (t < cost) cost = t, best = k;
   }
   return best;
@@ -687,17 +873,20 @@ cudaError_t launch_ssm_fwd_tc(const SsmParams &s, int nseg, void *workspace, cud
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && ready != dev) {
-    e = cudaFuncSetAttribute(ssm_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SsmSmem::BYTES);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(ssm_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SsmSmem::BYTES);
+    e = cudaFuncSetAttribute(ssm_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SsmSmem::BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(ssm_states_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, StSmem::BYTES);
     if (e == cudaSuccess) ready = dev;
   }
   if (e != cudaSuccess) return e;
   if (nseg > 1) {
-    ssm_tc_kernel<true><<<(unsigned)items, 896, SsmSmem::BYTES, st>>>(p);
+    ssm_states_kernel<<<(unsigned)items, 608, StSmem::BYTES, st>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    ssm_fold_kernel<<<dim3((unsigned)(s.n_seqs * U), SSM_N * SSM_COLS / 1024), 256, 0, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  ssm_tc_kernel<false><<<(unsigned)((size_t)s.n_seqs * nseg * U), 896, SsmSmem::BYTES, st>>>(p);
+  ssm_tc_kernel<<<(unsigned)((size_t)s.n_seqs * nseg * U), 896, SsmSmem::BYTES, st>>>(p);
   return cudaGetLastError();
 }
 

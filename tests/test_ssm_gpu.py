@@ -379,3 +379,30 @@ def test_fp32_segments_and_steps_agree(kda):
         parts.append(yp)
     assert ref.rel(torch.cat(parts).cpu(), y.cpu().double()) <= 2 * TOL["f32"]
     assert ref.rel(h.cpu(), hT.cpu().double()) <= 2 * TOL["f32"]
+
+
+@pytest.mark.parametrize("lens,H,P", [([4100], 1, 64), ([2000, 1, 2100], 1, 128)])
+def test_segments_that_remember(kda, lens, H, P):
+    # hardly any decay: a state holds thousands of tokens, and what the first segment adds reaches the last
+    s = case(lens, H, 1, P, "bf16", 41)
+    x, b, c = split(s["rows"].cuda(), H, 1, P)
+    a = torch.full((H,), -1e-4)
+    y, hT = kda.ssm_fwd(x, s["dt"].cuda(), a.cuda(), b, c, s["cu"], s["h0"].cuda(), d_skip=s["d_skip"].cuda(), dt_bias=s["dt_bias"].cuda())
+    y_ref, h_ref = ref.scan(x, s["dt"], a, b, c, lens, s["h0"], s["d_skip"], s["dt_bias"])
+    assert ref.rel(y.float(), y_ref) <= TOL["bf16"] and ref.rel(hT, h_ref) <= TOL["f32"]
+
+
+def test_long_sums_keep_fp32(kda):
+    # all terms of one sign and no decay, 32768 of them: the tensor cores cut off up to 2^-23 of a sum at each of a chunk's 8 steps, on
+    # average half, and the chunks are added with rounding: below 4 * 2^-23 + 16 * 2^-24 < 2e-6 of the largest value, doubled
+    T, H = 32768, 40
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    f = lambda *s: torch.rand(*s, generator=gen, device="cuda")
+    x, b, c, dt = f(T, H, 64).bfloat16(), f(T, 1, 128).bfloat16(), f(T, 1, 128).bfloat16(), f(T, H) * 0.1 + 0.01
+    a = torch.full((H,), -1e-7, device="cuda")
+    _, hT = kda.ssm_fwd(x, dt, a, b, c, dt_softplus=False)
+    ha = dt.double() * a.double()
+    w = torch.exp(ha.flip(0).cumsum(0).flip(0) - ha) * dt.double()
+    for h in (0, 17, 39):
+        want = b[:, 0].double().t() @ (w[:, h, None] * x[:, h].double())
+        assert ref.rel(hT[0, h], want) <= 4e-6
