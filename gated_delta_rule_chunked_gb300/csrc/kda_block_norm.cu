@@ -674,12 +674,7 @@ cudaError_t launch_block_norm_bwd(const BlockNormParams &p, bool f32, cudaStream
   cudaError_t e = cudaLaunchKernelEx(&cfg, bwd_fn(l.lpr, gate_kind(p), p.residual && p.d_out && p.d_normed, f32), q);   // no rows: the partials become zero
   if (e != cudaSuccess) return e;
   if (!p.dw_post && !p.dscale && !p.dw_pre) return cudaSuccess;
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)((p.dim + 31) / 32));
-  cfg.blockDim = dim3(1024);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, block_norm_dw_kernel, p, l.ctas);
+  return launch_under(block_norm_dw_kernel, dim3((unsigned)((p.dim + 31) / 32)), 1024, 0, st, p, l.ctas);
 }
 
 }  // namespace kda

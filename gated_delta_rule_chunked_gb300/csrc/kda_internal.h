@@ -224,6 +224,22 @@ cudaError_t launch_cp_last(const float *hseg, int n_seqs, int P, int heads, floa
 // [N][L][C]), and the scan reads x, B and C from there; the pools advance in place.
 constexpr int SSM_N = 128;     // d_state
 constexpr int SSM_COLS = 64;   // value columns per CTA: a head of 128 takes two
+// fn<<<grid, threads, smem, s>>>(args...), let start while the kernel before it on the stream still runs (the kernels say what they wait for).
+template <typename... P, typename... A>
+cudaError_t launch_under(void (*fn)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
 struct SsmParams {
   int n_seqs, H, G, P;
   long long T;

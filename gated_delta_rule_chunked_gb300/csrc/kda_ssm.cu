@@ -180,6 +180,7 @@ struct Rec {
 template <int W, int TB, bool STATES>
 __global__ void __launch_bounds__(288) ssm_rec_kernel(SsmParams p, int nseg, float *seg_state, float *seg_decay) {
   typedef Rec<W, TB> R;
+  if (STATES) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __shared__ __align__(16) typename R::Smem sm;
   __shared__ __align__(16) float steps[2][2][TB];   // by batch: h, exp(h a)
   const int slices = p.P / W, head = blockIdx.x / slices, col0 = (blockIdx.x % slices) * W;
@@ -196,6 +197,7 @@ __global__ void __launch_bounds__(288) ssm_rec_kernel(SsmParams p, int nseg, flo
   f2 S2[R::R][2];
 #pragma unroll
   for (int i = 0; i < R::R; ++i) S2[i][0] = two(S[i][0], S[i][1]), S2[i][1] = two(S[i][2], S[i][3]);
+  if (!STATES && nseg > 1) asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the states' pass
   if (!STATES && !scalars)
 #pragma unroll 4
     for (int k = 0; k < seg; ++k) {
@@ -447,8 +449,9 @@ cudaError_t launch_rec(const SsmParams &p, const SsmRecPlan &l, void *workspace,
     ssm_rec_kernel<W, TB, true><<<dim3(slices, p.n_seqs * (l.nseg - 1)), 288, 0, s>>>(p, l.nseg, state, decay);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    return launch_under(ssm_rec_kernel<W, TB, false>, dim3(slices, p.n_seqs * l.nseg), 288, 0, s, p, l.nseg, state, decay);
   }
-  ssm_rec_kernel<W, TB, false><<<dim3(slices, p.n_seqs * l.nseg), 288, 0, s>>>(p, l.nseg, state, decay);
+  ssm_rec_kernel<W, TB, false><<<dim3(slices, p.n_seqs), 288, 0, s>>>(p, 1, state, decay);
   return cudaGetLastError();
 }
 cudaError_t launch_ssm_fwd_f32(const SsmParams &p, const SsmRecPlan &l, void *workspace, cudaStream_t s) {
@@ -462,16 +465,8 @@ cudaError_t launch_ssm_step(const SsmParams &p, bool f32, cudaStream_t s) {
   else ssm_conv_step_kernel<bf16><<<cgrid, 256, 0, s>>>(p, C);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(p.H * (p.P / SSM_COLS), p.n_seqs);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return f32 ? cudaLaunchKernelEx(&cfg, ssm_step_kernel<float>, p, C) : cudaLaunchKernelEx(&cfg, ssm_step_kernel<bf16>, p, C);
+  const dim3 grid(p.H * (p.P / SSM_COLS), p.n_seqs);
+  return f32 ? launch_under(ssm_step_kernel<float>, grid, 256, 0, s, p, C) : launch_under(ssm_step_kernel<bf16>, grid, 256, 0, s, p, C);
 }
 
 }  // namespace kda

@@ -374,6 +374,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
     f2 S[16];   // pairs of columns
     auto place = [&]() { return (((size_t)n * p.s.H + head) * SSM_N + row) * p.s.P + col0 + 32 * half; };   // of the row in h0 and hT
     const float *from = p.s.h0 ? p.s.h0 + place() : nullptr;
+    if (nseg > 1) asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the entering states; nothing else here depends on the kernels before
     if (seg > 0) from = p.seg_state + ((((size_t)n * (nseg - 1) + seg - 1) * U + u) * SSM_N + row) * SSM_COLS + 32 * half;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -629,6 +630,7 @@ __global__ void __launch_bounds__(608, 1) ssm_states_kernel(const __grid_constan
     if (threadIdx.x == 0) report(p.s.status, 3 /* KDA_ERR_CUDA */);
     return;
   }
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");   // the kernels after this one wait for its end where they read
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, row = tid & 127;
   const int U = p.s.H * (p.s.P / SSM_COLS), nseg = p.nseg;
   const int u = blockIdx.x % U, ns = blockIdx.x / U, seg = ns % (nseg - 1), n = ns / (nseg - 1);
@@ -800,6 +802,7 @@ __global__ void __launch_bounds__(256) ssm_fold_kernel(SsmTcParams p) {
   float4 v[MOST_SEGS - 1];
   float dec[MOST_SEGS - 1];
   auto place = [&](int k) { return reinterpret_cast<float4 *>(p.seg_state + (((size_t)n * m + k) * U + u) * SSM_N * SSM_COLS) + e; };
+  asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;\n" ::: "memory");
 #pragma unroll
   for (int k = 0; k < MOST_SEGS - 1; ++k)
     if (k < m) v[k] = *place(k), dec[k] = p.seg_decay[((size_t)n * m + k) * U + u];
@@ -882,11 +885,11 @@ cudaError_t launch_ssm_fwd_tc(const SsmParams &s, int nseg, void *workspace, cud
     ssm_states_kernel<<<(unsigned)items, 608, StSmem::BYTES, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    ssm_fold_kernel<<<dim3((unsigned)(s.n_seqs * U), SSM_N * SSM_COLS / 1024), 256, 0, st>>>(p);
-    e = cudaGetLastError();
+    e = launch_under(ssm_fold_kernel, dim3((unsigned)(s.n_seqs * U), SSM_N * SSM_COLS / 1024), 256, 0, st, p);
     if (e != cudaSuccess) return e;
+    return launch_under(ssm_tc_kernel, dim3((unsigned)((size_t)s.n_seqs * nseg * U)), 896, SsmSmem::BYTES, st, p);
   }
-  ssm_tc_kernel<<<(unsigned)((size_t)s.n_seqs * nseg * U), 896, SsmSmem::BYTES, st>>>(p);
+  ssm_tc_kernel<<<(unsigned)((size_t)s.n_seqs * U), 896, SsmSmem::BYTES, st>>>(p);
   return cudaGetLastError();
 }
 
