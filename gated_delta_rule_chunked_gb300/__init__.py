@@ -9,6 +9,11 @@ ctypes, and turns status codes into exceptions.
     grads = kda_bwd(q, k, v, beta, g, dO, saved, cu_seqlens, h0, dhT)
     o = kda_step(q, k, v, beta, g, state, accept_len)     # state updated in place
 
+and what stands around a recurrent layer: the selective scan behind its short convolution
+(``ssm_fwd`` for prompts, ``ssm_step`` for decoding), the verification of drafted tokens
+(``draft_verify``), and the norms, gate and residual sum around a block (``block_norm_fwd``,
+``block_norm_bwd``). examples/draft_decode.py runs them together.
+
 Shapes: q, k, v, g, dO [total, H, 128]; beta [total, H]; states [N, H, 128, 128]
 (fp32, [key][value]); decode inputs carry an extra step axis: [N, L, H, ...].
 """

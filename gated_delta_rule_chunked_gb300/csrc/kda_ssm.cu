@@ -6,9 +6,12 @@
 // One CTA owns 64 (or 16) value columns of one (sequence, head): 256 threads hold the 128 x 64 state in
 // registers, each 8 rows x 4 columns (16 lanes cover a row's 64 columns, so states move as whole 256-byte
 // rows). Per token a thread reads 8 values of B, 8 of C and 4 of x from shared memory for 96 operations;
-// the sums over the row groups meet once per 8 tokens.
-// Step: bound by reading and writing the 32 KB state. The convolution runs as a kernel of its own
-// (its state is shared by every head of a group, so it cannot be advanced in place by the heads'
+// the sums over the row groups meet once per batch of tokens. No product goes through the tensor cores, whose
+// operands would not hold 24 bits. Prompts are bound by the issue of those products and sums (52% of the issue
+// slots at two warps a scheduler; 2048 tokens x 96 heads of 64 in 410 us).
+// Step: bound by reading and writing the 32 KB state (256 sequences x 4 slots x 96 heads of 64, 1.66 GB:
+// 295 us, 5.6 TB/s, when every sequence commits; 258 us at drawn prefixes, of which some commit nothing). The convolution runs as a kernel of
+// its own (its state is shared by every head of a group, so it cannot be advanced in place by the heads'
 // CTAs), and the scan starts under it (programmatic dependent launch): it has its state in
 // registers by the time the convolution's rows are there.
 #include "kda_common.cuh"
@@ -431,7 +434,7 @@ SsmRecPlan ssm_rec_plan(int n_seqs, long long T, int H, int P) {
     const double m = (double)((n + sms - 1) / sms);
     return l.cols == 16 && m > 1 ? 0.87 * m : m;
   };
-  double cost = each * walk(ctas);
+  double cost = 0.9 * each * walk(ctas);   // less than a tenth to gain is left alone: 2048 tokens x 96 heads of 64 410 us, 433 in 11 segments
   for (int k = 2; k <= 16 && 16 * k <= each && (long long)n_seqs * k <= 65535; ++k) {
     const double t = 1.5 * each / k * walk(ctas * k) + 30.0 + 2.0 * k;
     if (t < cost) cost = t, l.nseg = k;

@@ -379,12 +379,14 @@ kda_status kda_conv_step(const kda_conv_step_args *args, cudaStream_t stream);
  * 2 * groups * d_state channels, and are read in place through their row strides.
  *  - d_state = 128; head_dim 64 or 128; groups divides heads; a <= 0 is expected.
  *  - Row strides (ld*, in elements) must be multiples of 8 and at least the row's width.
- *  - Inputs are finite. A sequence's outputs depend on that sequence's rows only.
+ *  - Inputs are finite. A sequence's outputs depend on that sequence's rows only; rows outside every
+ *    sequence are left as they are. y and hT overlap no input.
  * bf16 I/O: the products run on the tensor cores in chunks of 128 tokens; the state, the
  * decays and all sums are fp32. The state update splits its fp32 factor into three bf16 terms
- * (error 2^-24 of a term). The decay-weighted scores of a chunk are rounded to bf16 once before
- * their product with x, which costs y about as much as its own rounding to bf16. fp32 I/O runs
- * in fp32 on the CUDA cores.
+ * (error 2^-24 of a term). The decay-weighted scores of a chunk, and the copy of the state that a
+ * chunk's outputs read, are rounded to bf16 once, which costs y about as much as its own rounding
+ * to bf16. fp32 I/O runs in fp32 on the CUDA cores. Sequences with few heads run in segments in
+ * either type, through a workspace; without one the size is 0.
  */
 typedef struct {
     int32_t n_seqs;            /* N >= 0                                                 */
