@@ -572,10 +572,12 @@ Kernel bwd_fn(int lpr, int gate, bool full, bool f32) {
   return gate == GATE_NONE ? bwd_fn<bf16, GATE_NONE>(lpr, full) : gate == GATE_SILU ? bwd_fn<bf16, GATE_SILU>(lpr, full) : bwd_fn<bf16, GATE_SIGMOID>(lpr, full);
 }
 
-// The backward's launch. Long rows: as few CTAs per row as 256 threads of 8 columns allow (1, 2, 4 or 8); three to
-// six buffers, as many as leave room for two CTAs per SM. The count of CTAs sizes the workspace, so it
-// goes by the sizes alone: the gate's kernels are taken to hold as many at once as the SiLU's.
-constexpr int BWD_RING = 3 * 5 * 256 * 8 * (int)sizeof(float);   // the largest ring: three rows of 256 threads' fp32 columns
+// The backward's launch. Long rows: as few CTAs per row (of 1 to 8) as keep nearly the most columns on an SM that any count does
+// (bf16: 5120 columns in 4 of 160 threads 5.2 TB/s, in 4 that fill two thirds of an SM 4.1; 6144 in 3 of 256 5.2, in 4 of 192
+// 4.9; 7168 in 4 of 224 5.0, in 7 of 128, a seventh more, 4.9). In fp32 a CTA takes up to 128 threads, whose rows leave room for others
+// (2048 columns in 2 of 128 5.4 TB/s, in one of 256 3.7). Three to six buffers, as many as leave room for the SM's CTAs. The
+// count of CTAs sizes the workspace, so it goes by the sizes alone: the gate's kernels are taken to hold as many at once as the SiLU's.
+constexpr int BWD_RING = 216 * 1024;   // the rings of an SM's CTAs together
 struct BwdLaunch {
   int lpr, threads, cluster, stages, ctas;   // ctas: rows of partials
   size_t smem;
@@ -608,13 +610,22 @@ BwdLaunch bwd_launch(long long rows, int dim, bool f32) {
     groups = (rows + rpc - 1) / rpc;
   } else {
     const int nvec = dim / 8;
-    int cl = 1;
-    while (nvec > 256 * cl) cl *= 2;
-    const int per = (nvec + cl - 1) / cl;
-    const size_t buffer = (size_t)5 * per * 8 * (f32 ? 4 : 2);
-    int stages = (int)(108 * 1024 / buffer);   // at most BWD_RING bytes, also where three take more
-    stages = stages < 3 ? 3 : (stages > 6 ? 6 : stages);
-    l = {0, (per + 31) / 32 * 32, cl, stages, 0, stages * buffer};
+    const int most = f32 && nvec <= 1024 ? 128 : 256;
+    struct Cut {
+      int per, threads, ctas;   // vectors and threads of a CTA, CTAs on an SM by registers (128 a thread) and a ring of three rows
+    };
+    auto cut = [&](int cl) -> Cut {
+      const int per = (nvec + cl - 1) / cl, threads = (per + 31) / 32 * 32, row = 5 * per * 8 * (f32 ? 4 : 2);
+      if (per > most || (cl - 1) * per >= nvec || (cl > 1 && per < 64)) return {0, 0, 0};   // one or two warps: 1544 in bf16 3.9 TB/s, in one CTA 4.7
+      const int ctas = 512 / threads < BWD_RING / (3 * row) ? 512 / threads : BWD_RING / (3 * row);
+      return {per, threads, ctas};
+    };
+    int best = 0, cl = 1;
+    for (int k = 1; k <= 8; ++k) best = cut(k).ctas * cut(k).per > best ? cut(k).ctas * cut(k).per : best;
+    while (cut(cl).ctas * cut(cl).per < 0.87 * best) ++cl;
+    const Cut c = cut(cl);
+    const int row = 5 * c.per * 8 * (f32 ? 4 : 2), fit = BWD_RING / c.ctas / row, stages = fit > 6 ? 6 : fit;
+    l = {0, c.threads, cl, stages, 0, (size_t)stages * row};
     for (int k = 0; ask && k < 6 && e == cudaSuccess; ++k)
       e = cudaFuncSetAttribute(bwd_fn(0, k / 2, k % 2, f32), cudaFuncAttributeMaxDynamicSharedMemorySize, BWD_RING);   // not l.smem: other sizes use the same kernels
     cudaLaunchConfig_t cfg = {};
