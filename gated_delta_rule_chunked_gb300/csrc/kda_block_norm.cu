@@ -9,7 +9,7 @@
 //   t = dx scale w_post,  dz = t hat act'(z),  dhat = t act(z),  du = r_u (dhat - hat mean(dhat hat))
 // (dhat hat = dx m summed over a row, with m = scale w_post h)
 // Memory-bound: every tensor is read and written once, everything in between is fp32 registers. In bf16 the forward
-// moves 2.35 GB at 32768 x 7168 in 0.391 ms (6.0 TB/s, 89% of a copy) and 0.30 GB at 393216 x 128 in 51 us (5.9 TB/s); the
+// moves 2.35 GB at 32768 x 7168 in 0.356 ms (6.6 TB/s, 97% of a copy) and 0.30 GB at 393216 x 128 in 51 us (5.9 TB/s); the
 // backward moves 1.88 GB at 16384 x 7168 in 0.367 ms (5.1 TB/s): it keeps 14 warps on an SM, whose registers the sums over rows
 // and the column vectors fill, and issues in 55% of the slots.
 // Forward: a row is owned by LPR lanes of a warp (short rows) or by a whole CTA (LPR = 0), each thread
@@ -211,9 +211,17 @@ struct BwdRow {   // what the second half of a row needs of the first, beside u 
   }
 };
 
+// CTAs of 512 threads on an SM, which bounds the registers: a row waits twice for its sums, and only other rows fill those times
+// (one CTA more: 32768 x 7168 bf16 0.391 -> 0.356 ms, fp32 5.5 -> 6.8 TB/s; 16384 columns bf16 4.9 -> 6.2 TB/s). In fp32 with
+// four vectors a thread a second one would spill.
+template <typename IO>
+constexpr int fwd_ctas(int lpr, int vpt) {
+  if (lpr || vpt == 1) return 0;   // no bound: they hold few registers by themselves, and take more where one CTA is asked for
+  return sizeof(IO) == 2 ? (vpt == 2 ? 3 : 2) : (vpt == 2 ? 2 : 1);
+}
 // One row per (CTA or LPR lanes); the grid covers all rows.
 template <typename IO, int GATE, int LPR, int VPT>
-__global__ void __launch_bounds__(LPR ? 256 : 512) block_norm_fwd_kernel(BlockNormParams p) {
+__global__ void __launch_bounds__(LPR ? 256 : 512, fwd_ctas<IO>(LPR, VPT)) block_norm_fwd_kernel(BlockNormParams p) {
   __shared__ float red[64];
   const int lane = LPR ? (threadIdx.x & (LPR - 1)) : threadIdx.x, step = LPR ? LPR : blockDim.x;
   const int nvec = p.dim >> 3;
@@ -660,12 +668,12 @@ cudaError_t launch_block_norm_fwd(const BlockNormParams &p, bool f32, cudaStream
   const Shape s = shape(p.dim);
   const int rpc = s.lpr ? s.threads / s.lpr : 1;
   const Kernel fn = fwd_fn(s, gate_kind(p), f32);
-  // about half the CTAs that the device holds at once (a quarter to one and a half of them measured within 2%;
-  // 0.434 -> 0.394 ms at 32768 x 7168, 0.228 -> 0.210 ms at 65536 x 2048; two waves are slower)
+  // about a quarter to a third of the CTAs that the device holds at once (twice as far costs up to 2% in bf16, 15% at 16384 columns of
+  // fp32, four times as far more; without it 0.434 instead of 0.394 ms at 32768 x 7168 before the third CTA)
   BlockNormParams q = p;
   int dev = 0, sms = 0;
   if (!s.lpr && cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
-    q.prefetch_dist = sms * (1024 / s.threads);
+    q.prefetch_dist = sms * (512 / s.threads);
   fn<<<(unsigned)((p.rows + rpc - 1) / rpc), s.threads, 0, st>>>(q);
   return cudaGetLastError();
 }
