@@ -273,7 +273,8 @@ cudaError_t launch_ssm_fwd_f32(const SsmParams &p, const SsmRecPlan &l, void *wo
 struct SsmTcParams {
   CUtensorMap tm_x, tm_b, tm_c, tm_y;   // [T][row], boxes of 64 columns x 128 tokens, 128-byte swizzle
   SsmParams s;
-  int nseg, sorted;   // sorted: CTAs take the sequences by falling length
+  int nseg, sorted;   // sorted: the sequences are taken by falling length
+  unsigned items;     // sequences x segments x units
   float *seg_state, *seg_decay;
 };
 int ssm_segments(int n_seqs, long long T, int units);

@@ -5,7 +5,7 @@
 //   M  = G o 2^(c_i - c_j) h_j  (j <= i, else 0)
 //   Y  = M X + diag(2^c_i) C S + d X
 //   S' = 2^c_last S + B^T (w o X),   w_j = 2^(sum_{k > j} h_k a log2 e) h_j
-// One CTA owns 64 value columns of one (sequence, head) and walks its chunks; the state stays in the
+// One CTA owns 64 value columns of one (sequence, head) at a time and walks its chunks; the state stays in the
 // registers of one warpgroup (thread = state channel), so the chain between chunks is one multiply-add
 // per element. Roles (28 warps; a role's eight warps are two per 32 rows, each with half of the columns,
 // because the work per thread is short chains that one warp per scheduler cannot fill):
@@ -46,7 +46,8 @@ struct SsmSmem {
   static constexpr int BAR = SC + 4 * Q * 4;
   static constexpr int BARS = 40;            // places for the barriers
   static constexpr int TSLOT = BAR + BARS * 8;
-  static constexpr int BYTES = TSLOT + 16;
+  static constexpr int ORDER = TSLOT + 16;   // the sequences by falling length
+  static constexpr int BYTES = ORDER + 256 * 2;
 };
 static_assert(SsmSmem::BYTES <= 232448, "shared memory of one SM");
 
@@ -136,11 +137,9 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo) { return (uint64_t)(64u | 
 // Byte offset of 16-byte chunk k of row r in a [rows][64] bf16 tile with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t row_chunk(int r, int k) { return (uint32_t)(r * 128 + ((k ^ (r & 7)) << 4)); }
 
-// Sequence number r of the sequences by falling length (at most MOST_SORTED, one thread each). CTAs start in the order of
-// their numbers, so the longest go first and none of them is left running alone at the end (eight packed prompts whose
-// longest is the last one: 0.211 -> 0.187 ms).
+// The sequences by falling length, at most MOST_SORTED.
 constexpr int MOST_SORTED = 256;
-__device__ __forceinline__ int nth_longest(const int *cu, int n_seqs, int r, int *scratch) {
+__device__ __forceinline__ void sort_longest(const int *cu, int n_seqs, int *scratch, uint16_t *order) {
   const int t = threadIdx.x;
   if (t < n_seqs) scratch[t] = cu[t + 1] - cu[t];
   __syncthreads();
@@ -148,11 +147,64 @@ __device__ __forceinline__ int nth_longest(const int *cu, int n_seqs, int r, int
     const int len = scratch[t];
     int rank = 0;
     for (int j = 0; j < n_seqs; ++j) rank += scratch[j] > len || (scratch[j] == len && j < t);
-    if (rank == r) scratch[MOST_SORTED] = t;
+    order[rank] = (uint16_t)t;
   }
   __syncthreads();
-  return scratch[MOST_SORTED];
 }
+// One item of the launch: the token a chunk before its first, its chunks, its unit, and sequence | segment << 16 | the last chunk's tokens << 20.
+__device__ __forceinline__ int4 item_of(const SsmTcParams *p, const uint16_t *order, int i) {
+  const int U = p->s.H * (p->s.P / SSM_COLS), u = i % U, ns = i / U, seg = ns % p->nseg;
+  int n = ns / p->nseg;
+  if (p->sorted) n = order[n];
+  // token indices fit 32 bits (T < 2^31), and offsets that are no sequence's are taken as an empty one
+  const int each = (int)(p->s.T / p->s.n_seqs), seq0 = max(p->s.cu ? p->s.cu[n] : each * n, 0);
+  const int seq1 = max(min(p->s.cu ? p->s.cu[n + 1] : each * (n + 1), (int)p->s.T), seq0);
+  const int all = (int)(((unsigned)(seq1 - seq0) + Q - 1) / Q), first = (int)((long long)all * seg / p->nseg), last = (int)((long long)all * (seg + 1) / p->nseg);
+  return make_int4(seq0 + (first - 1) * Q, last - first, u, n | seg << 16 | min(seq1 - seq0 - (last - 1) * Q, Q) << 20);
+}
+// Kept out of line: its divisions in every role's loop push the roles' code out of the instruction cache.
+__device__ __noinline__ int4 item_at(const SsmTcParams *p, const uint16_t *order, int i) { return item_of(p, order, i); }
+// A CTA's way through its items (sequence, segment, unit) and their chunks, the same for every role. Items are dealt out from the longest
+// sequence on, forwards and backwards in turn, so that the CTAs end about together.
+// Without MANY a CTA has one.
+template <bool MANY>
+struct Walk {
+  int round = 0, left = 0;   // chunks of the item after this one
+  int t, u = 0, what;            // the chunk's first token; unit; the rest as item_at gives it
+  bool fresh;                // the chunk is an item's first
+  __device__ __forceinline__ Walk(const SsmTcParams &p, const uint16_t *order) {
+    if (MANY) return;
+    const int4 v = item_of(&p, order, (int)blockIdx.x);
+    t = v.x, left = v.y, u = v.z, what = v.w;
+  }
+  __device__ __forceinline__ bool item(const SsmTcParams &p, const uint16_t *order) {   // the next one, which may be empty
+    if (!MANY) return ++round == 1;
+    const int G = (int)gridDim.x, b = (int)blockIdx.x, i = round * G + (round & 1 ? G - 1 - b : b);   // below 2^31: at most one round past the items
+    if ((unsigned)i >= p.items) return false;
+    ++round;
+    const int4 v = item_at(&p, order, i);
+    t = v.x, left = v.y, u = v.z, what = v.w;
+    return true;
+  }
+  __device__ __forceinline__ bool chunk(const SsmTcParams &p, const uint16_t *order) {
+    if (!MANY) {
+      fresh = round == 0, round = 1;
+      if (left == 0) return false;
+    } else {
+      fresh = left == 0;
+      while (left == 0)
+        if (!item(p, order)) return false;
+    }
+    --left;
+    t += Q;
+    return true;
+  }
+  __device__ __forceinline__ int len() const { return left == 0 ? what >> 20 : Q; }
+  __device__ __forceinline__ int seq() const { return what & 0xffff; }
+  __device__ __forceinline__ int seg() const { return what >> 16 & 15; }
+  __device__ __forceinline__ int head(const SsmTcParams &p) const { return p.s.P == SSM_COLS ? u : u >> 1; }
+  __device__ __forceinline__ int col0(const SsmTcParams &p) const { return p.s.P == SSM_COLS ? 0 : (u & 1) * SSM_COLS; }
+};
 
 // w times half of a token's X as three bf16 tiles: 24 bits in truncated terms of 8, so the remainders are exact.
 __device__ __forceinline__ void weigh(const char *x, char *wx, int row, int half, float w) {
@@ -190,6 +242,7 @@ __device__ __forceinline__ float forgets(float h, float al) {
   return l < -200.f ? -200.f : l;
 }
 
+template <bool MANY>
 __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ SsmTcParams p) {
   using L = SsmSmem;
   extern __shared__ __align__(1024) char smem[];
@@ -199,17 +252,8 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
   }
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, row = tid & 127;
   const int role = warp >> 3, half = (warp >> 2) & 1, wq = warp & 3;   // eight warps per role, two per 32 rows
-  const int U = p.s.H * (p.s.P / SSM_COLS), nseg = p.nseg;
-  const int u = blockIdx.x % U, ns = blockIdx.x / U, seg = ns % nseg;
-  const int n = p.sorted ? nth_longest(p.s.cu, p.s.n_seqs, ns / nseg, reinterpret_cast<int *>(smem)) : ns / nseg;
-  const int head = u / (p.s.P / SSM_COLS), col0 = (u % (p.s.P / SSM_COLS)) * SSM_COLS, group = head / (p.s.H / p.s.G);
-  // token indices fit 32 bits (T < 2^31)
-  // and offsets that are no sequence's are taken as an empty one
-  const int each = (int)(p.s.T / p.s.n_seqs), seq0 = max(p.s.cu ? p.s.cu[n] : each * n, 0);
-  const int seq1 = max(min(p.s.cu ? p.s.cu[n + 1] : each * (n + 1), (int)p.s.T), seq0);
-  const int all = (int)(((unsigned)(seq1 - seq0) + Q - 1) / Q);
-  const int first = (int)((long long)all * seg / nseg), nch = (int)((long long)all * (seg + 1) / nseg) - first;
-  const int t_begin = seq0 + first * Q;
+  uint16_t *order = reinterpret_cast<uint16_t *>(smem + L::ORDER);
+  if (p.sorted) sort_longest(p.s.cu, p.s.n_seqs, reinterpret_cast<int *>(smem), order);
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + L::BAR);
   uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + L::TSLOT);
   float *sc_c = reinterpret_cast<float *>(smem + L::SC), *sc_h = sc_c + Q, *sc_w = sc_h + Q, *sc_e = sc_w + Q;
@@ -233,26 +277,26 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tslot, tl = tmem + ((uint32_t)(32 * wq) << 16);
-  auto len_of = [&](int c) -> int {
-    return min(seq1 - (t_begin + c * Q), Q);
-  };
   bool ok = true;
-  int c = 0;
+  Walk<MANY> w(p, order);
+  int c = 0;   // chunks so far, of all items: the barriers' phases go by it
 
   if (role == 0) {
-    // ------------------------------------------------------------ M and Y
+    // -------------------------------------------------------------- M and Y
     {
       const uint32_t z[8] = {};
 #pragma unroll 1
       for (int k = half; k < 8; k += 2) st8u(tl + T_M + 8 * k, z);   // blocks above the diagonal stay zero
       tc::wait_st();
     }
-    const float d = p.s.d_skip ? p.s.d_skip[head] : 0.f;
-    const f2 d2 = two(d, d);
-    f2 e2 = two(0.f, 0.f);
-    for (c = 0; c <= nch; ++c) {
+    f2 e2 = two(0.f, 0.f), d2 = e2;
+    int len = 0, t = 0, u = 0;   // of the previous chunk
+    float d = !MANY && p.s.d_skip ? p.s.d_skip[w.head(p)] : 0.f;
+    if (!MANY) d2 = two(d, d);
+    for (;; ++c) {
+      const bool more = w.chunk(p, order);
       if (c > 0) {   // the previous chunk's Y, while this chunk's G runs
-        const int k0 = c - 1, len = len_of(k0);
+        const int k0 = c - 1;
         char *ys = smem + (k0 & 1) * L::STAGE + L::X;   // in the place of the chunk's X, which everything has read by then
         ok = mbar_wait_quiet(&bar[YDONE], k0 & 1) && mbar_wait_quiet(&bar[XEMPTY0 + (k0 & 1)], (k0 >> 1) & 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -279,16 +323,18 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
         }
         tc::fence_before();
         mbar_arrive(&bar[YFREE]);
-        fence_proxy_async();
-        mbar_arrive(&bar[YSTAGED0 + (k0 & 1)]);
-        if (len < Q && row < len) {   // a short last chunk: its box would reach into the next sequence
-          bf16 *out = static_cast<bf16 *>(p.s.y) + ((long long)(t_begin + k0 * Q + row) * p.s.H + head) * p.s.P + col0;
+        if (len < Q && row < len) {   // a sequence's short last chunk: its box would reach into the next sequence
+          bf16 *to = static_cast<bf16 *>(p.s.y) + (long long)(t + row) * p.s.H * p.s.P + u * SSM_COLS;
 #pragma unroll 1
           for (int k = 4 * half; k < 4 * half + 4; ++k)
-            *reinterpret_cast<uint4 *>(out + 8 * k) = *reinterpret_cast<const uint4 *>(ys + row_chunk(row, k));
+            *reinterpret_cast<uint4 *>(to + 8 * k) = *reinterpret_cast<const uint4 *>(ys + row_chunk(row, k));   // the thread's own
         }
+        fence_proxy_async();
+        mbar_arrive(&bar[YSTAGED0 + (k0 & 1)]);
       }
-      if (c == nch) break;
+      if (!more) break;
+      len = w.len(), t = w.t, u = w.u;
+      if (MANY && w.fresh && p.s.d_skip) d = p.s.d_skip[w.head(p)];
       // M's columns are free: the products of the previous chunk were issued before this G
       ok = mbar_wait_quiet(&bar[SFULL], c & 1) && mbar_wait_quiet(&bar[GDONE], c & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -342,17 +388,20 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
       mbar_arrive(&bar[SEMPTY]);
       const float ei = exp2f(ci);
       e2 = two(ei, ei);
+      if (MANY) d2 = two(d, d);
     }
   } else if (role == 1) {
     // -------------------------------------------------------------- w o X
-    for (c = 0; c < nch; ++c) {
+    for (; w.chunk(p, order); ++c) {
       char *st = smem + (c & 1) * L::STAGE;
-      ok = ok && mbar_wait_quiet(&bar[SFULL], c & 1) && mbar_wait_quiet(&bar[XFULL0 + (c & 1)], (c >> 1) & 1);
+      ok = mbar_wait_quiet(&bar[SFULL], c & 1) && mbar_wait_quiet(&bar[XFULL0 + (c & 1)], (c >> 1) & 1);
       if (!ok) break;
-      const bool live = row < len_of(c);
-      const float w = live ? sc_w[row] : 0.f;
-      if (len_of(c) < Q) {
-        ok = mbar_wait_quiet(&bar[FULL0 + (c & 1)], (c >> 1) & 1);   // the only chunk at which this role waits for B: the sequence's last
+      const int len = w.len();
+      const bool live = row < len;
+      const float weight = live ? sc_w[row] : 0.f;
+      if (len < Q) {
+        // the only chunk at which this role waits for B, a sequence's last; the one before in this stage has been used up, or X would not be here
+        ok = mbar_wait_quiet(&bar[FULL0 + (c & 1)], (c >> 1) & 1);
         if (!ok) break;
         if (!live) {   // rows past the sequence's end belong to another one, or to nobody: whatever they hold stays out
           const uint4 z = make_uint4(0u, 0u, 0u, 0u);
@@ -367,7 +416,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
       }
       if (c > 0) ok = mbar_wait_quiet(&bar[DSPART0 + wq], (c - 1) & 1);   // the previous terms of these tokens are read
       if (!ok) break;
-      weigh(st + L::X, smem + L::WX, row, half, w);
+      weigh(st + L::X, smem + L::WX, row, half, weight);
       fence_proxy_async();
       mbar_arrive(&bar[WXREADY0 + wq]);
       mbar_arrive(&bar[XEMPTY0 + (c & 1)]);
@@ -376,76 +425,78 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
   } else if (role == 2) {
     // -------------------------------------------------------------- the state: row n of [128][64], 32 columns
     f2 S[16];   // pairs of columns
-    auto place = [&]() { return (((size_t)n * p.s.H + head) * SSM_N + row) * p.s.P + col0 + 32 * half; };   // of the row in h0 and hT
-    const float *from = p.s.h0 ? p.s.h0 + place() : nullptr;
-    if (nseg > 1) asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the entering states; nothing else here depends on the kernels before
-    if (seg > 0) from = p.seg_state + ((((size_t)n * (nseg - 1) + seg - 1) * U + u) * SSM_N + row) * SSM_COLS + 32 * half;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 v = from ? *reinterpret_cast<const float4 *>(from + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
-      S[2 * i] = two(v.x, v.y), S[2 * i + 1] = two(v.z, v.w);
-    }
-    auto put = [&]() {   // the operand tile
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint4 *>(smem + L::S + row_chunk(row, 4 * half + k)) =
-            make_uint4(pack2(S[4 * k]), pack2(S[4 * k + 1]), pack2(S[4 * k + 2]), pack2(S[4 * k + 3]));
-      fence_proxy_async();
-      mbar_arrive(&bar[SREADY]);
-    };
-    put();
-    for (c = 0; c < nch; ++c) {
-      ok = mbar_wait_quiet(&bar[SFULL], c & 1);
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      const float last = sc_c[Q - 1];
-      mbar_arrive(&bar[SEMPTY]);
-      const float dec = exp2f(last);
-      const f2 dec2 = two(dec, dec);
-      ok = mbar_wait_quiet(&bar[DSDONE], c & 1);
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      tc::fence_after();
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {   // 8 columns at a time: the registers hold no more
-        float d0[8], d1[8], d2[8];
-        ld8(tl + T_DS + 32 * half + 8 * k, d0);
-        ld8(tl + T_DS + 64 + 32 * half + 8 * k, d1);
-        ld8(tl + T_DS + 128 + 32 * half + 8 * k, d2);
-        tc::wait_ld();
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          S[4 * k + i] = fma2(S[4 * k + i], dec2, add2(two(d0[2 * i], d0[2 * i + 1]), add2(two(d1[2 * i], d1[2 * i + 1]), two(d2[2 * i], d2[2 * i + 1]))));
-      }
-      tc::fence_before();
-      mbar_arrive(&bar[DSFREE]);
-      if (c + 1 < nch) {
-        ok = mbar_wait_quiet(&bar[YDONE], c & 1);   // C S has read the previous operand
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        put();
-      }
-    }
-    if (ok && p.s.hT && seg == nseg - 1)
+    if (p.nseg > 1) asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the entering states; nothing else here depends on the kernels before
+    while (ok && w.item(p, order)) {
+      auto place = [&]() { return (((size_t)w.seq() * p.s.H + w.head(p)) * SSM_N + row) * p.s.P + w.col0(p) + 32 * half; };   // of the row in h0 and hT
+      const float *from = p.s.h0 ? p.s.h0 + place() : nullptr;
+      if (w.seg() > 0)
+        from = p.seg_state + ((((size_t)w.seq() * (p.nseg - 1) + w.seg() - 1) * (p.s.H * (p.s.P / SSM_COLS)) + w.u) * SSM_N + row) * SSM_COLS + 32 * half;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float2 a = of2(S[2 * i]), b = of2(S[2 * i + 1]);
-        *reinterpret_cast<float4 *>(p.s.hT + place() + 4 * i) = make_float4(a.x, a.y, b.x, b.y);
+        const float4 v = from ? *reinterpret_cast<const float4 *>(from + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        S[2 * i] = two(v.x, v.y), S[2 * i + 1] = two(v.z, v.w);
       }
+      for (; w.left > 0; --w.left, ++c) {
+        if (c > 0) {
+          ok = mbar_wait_quiet(&bar[YDONE], (c - 1) & 1);   // C S has read the previous operand
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)   // the operand tile
+          *reinterpret_cast<uint4 *>(smem + L::S + row_chunk(row, 4 * half + k)) =
+              make_uint4(pack2(S[4 * k]), pack2(S[4 * k + 1]), pack2(S[4 * k + 2]), pack2(S[4 * k + 3]));
+        fence_proxy_async();
+        mbar_arrive(&bar[SREADY]);
+        ok = mbar_wait_quiet(&bar[SFULL], c & 1);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const float last = sc_c[Q - 1];
+        mbar_arrive(&bar[SEMPTY]);
+        const float dec = exp2f(last);
+        const f2 dec2 = two(dec, dec);
+        ok = mbar_wait_quiet(&bar[DSDONE], c & 1);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc::fence_after();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {   // 8 columns at a time: the registers hold no more
+          float d0[8], d1[8], d2[8];
+          ld8(tl + T_DS + 32 * half + 8 * k, d0);
+          ld8(tl + T_DS + 64 + 32 * half + 8 * k, d1);
+          ld8(tl + T_DS + 128 + 32 * half + 8 * k, d2);
+          tc::wait_ld();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            S[4 * k + i] = fma2(S[4 * k + i], dec2, add2(two(d0[2 * i], d0[2 * i + 1]), add2(two(d1[2 * i], d1[2 * i + 1]), two(d2[2 * i], d2[2 * i + 1]))));
+        }
+        tc::fence_before();
+        mbar_arrive(&bar[DSFREE]);
+      }
+      if (ok && p.s.hT && w.seg() == p.nseg - 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 a = of2(S[2 * i]), b = of2(S[2 * i + 1]);
+          *reinterpret_cast<float4 *>(p.s.hT + place() + 4 * i) = make_float4(a.x, a.y, b.x, b.y);
+        }
+    }
   } else if (warp == 24) {
     // -------------------------------------------------------------- scalars: lane l has tokens 4 l .. 4 l + 3
-    const float al = p.s.a[head] * LOG2E, bias = p.s.dt_bias ? p.s.dt_bias[head] : 0.f;
-    auto fetch = [&](int k, float (&v)[4]) {
-      const int len = len_of(k);
+    float v[4], al = 0.f, bias = 0.f;
+    if (!MANY) al = p.s.a[w.head(p)] * LOG2E, bias = p.s.dt_bias ? p.s.dt_bias[w.head(p)] : 0.f;
+    auto fetch = [&]() {
+      const int len = w.len(), head = w.head(p);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = 4 * lane + i;
-        v[i] = t < len ? p.s.dt[(long long)(t_begin + k * Q + t) * p.s.H + head] : 0.f;
+        v[i] = t < len ? p.s.dt[(long long)(w.t + t) * p.s.H + head] : 0.f;
       }
     };
-    float v[4];
-    if (nch > 0) fetch(0, v);
-    for (c = 0; c < nch; ++c) {
-      const int len = len_of(c);
+    bool more = w.chunk(p, order);
+    if (more) fetch();
+    for (; more; ++c) {
+      const int len = w.len();
+      if (MANY && w.fresh) al = p.s.a[w.head(p)] * LOG2E, bias = p.s.dt_bias ? p.s.dt_bias[w.head(p)] : 0.f;
       float h[4] = {v[0], v[1], v[2], v[3]};
-      if (c + 1 < nch) fetch(c + 1, v);
+      more = w.chunk(p, order);
+      if (more) fetch();
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {   // one body for the four: the values rotate
         const float x = step_of(h[0], bias, p.s.softplus);
@@ -490,40 +541,44 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
   } else if (warp == 27) {
     // -------------------------------------------------------------- loads
     if (lane == 0) {
-      int issued = 0, xissued = 0;
-      // chunk k's outputs leave as one box from the place of its X tile
-      auto store = [&](int k) {
-        if (!mbar_wait_quiet(&bar[YSTAGED0 + (k & 1)], (k >> 1) & 1)) return false;
-        if (len_of(k) == Q) {
-          tma_store_2d(&p.tm_y, head * p.s.P + col0, t_begin + k * Q, smem + (k & 1) * L::STAGE + L::X);
-          bulk_commit();
-          bulk_wait_read();
-        }
-        return true;
-      };
+      int issued = 0, xissued = 0, group = MANY ? 0 : w.head(p) / (p.s.H / p.s.G);
+      int y_last = 0, x_last = 0, y_before = 0, x_before = 0;   // boxes of the last two chunks' outputs; -1: not by box
+      bool more = true;
 #pragma unroll 1
-      for (c = 0; c < nch + 2; ++c) {
+      for (int end = 0; end < 2; ++c) {
         char *st = smem + (c & 1) * L::STAGE;
-        const int t = t_begin + c * Q;
-        if (c < nch) {   // B and C first: they are free before Y has left from X's place
+        more = more && w.chunk(p, order);
+        end += !more;
+        const int x_col = w.u * SSM_COLS;
+        if (MANY && more && w.fresh) group = w.head(p) / (p.s.H / p.s.G);
+        if (more) {   // B and C first: they are free before Y has left from X's place
           if (c >= 2) ok = mbar_wait_quiet(&bar[EMPTY0 + (c & 1)], ((c >> 1) - 1) & 1);
           if (!ok) break;
           uint64_t *b = &bar[FULL0 + (c & 1)];
           mbar_expect_tx(b, 65536);
           for (int k = 0; k < 4; ++k)   // B's two halves, C's two
-            tc::tma_load_2d(st + (k < 2 ? L::B : L::C) + 16384 * (k & 1), k < 2 ? &p.tm_b : &p.tm_c, group * SSM_N + 64 * (k & 1), t, b);
+            tc::tma_load_2d(st + (k < 2 ? L::B : L::C) + 16384 * (k & 1), k < 2 ? &p.tm_b : &p.tm_c, group * SSM_N + 64 * (k & 1), w.t, b);
           issued = c + 1;
-          if (c + 1 < nch) {   // the next chunk's boxes into L2
-            for (int k = 0; k < 4; ++k) prefetch_2d(k < 2 ? &p.tm_b : &p.tm_c, group * SSM_N + 64 * (k & 1), t + Q);
-            prefetch_2d(&p.tm_x, head * p.s.P + col0, t + Q);
+          if (w.left > 0) {   // the next chunk's boxes into L2
+            for (int k = 0; k < 4; ++k) prefetch_2d(k < 2 ? &p.tm_b : &p.tm_c, group * SSM_N + 64 * (k & 1), w.t + Q);
+            prefetch_2d(&p.tm_x, x_col, w.t + Q);
           }
         }
-        if (c >= 2) ok = store(c - 2);
-        if (!ok) break;
-        if (c < nch) {
+        if (c >= 2) {   // the outputs of two chunks ago leave as one box from the place of their X tile
+          ok = mbar_wait_quiet(&bar[YSTAGED0 + (c & 1)], ((c >> 1) - 1) & 1);
+          if (!ok) break;
+          if (y_before >= 0) {
+            tma_store_2d(&p.tm_y, x_before, y_before, st + L::X);
+            bulk_commit();
+            bulk_wait_read();
+          }
+        }
+        x_before = x_last, y_before = y_last;
+        if (more) {
           mbar_expect_tx(&bar[XFULL0 + (c & 1)], 16384);
-          tc::tma_load_2d(st + L::X, &p.tm_x, head * p.s.P + col0, t, &bar[XFULL0 + (c & 1)]);
+          tc::tma_load_2d(st + L::X, &p.tm_x, x_col, w.t, &bar[XFULL0 + (c & 1)]);
           xissued = c + 1;
+          x_last = x_col, y_last = w.len() == Q ? w.t : -1;
         }
       }
       // every copy has landed, in either direction, before the CTA leaves, also after a timeout
@@ -540,11 +595,12 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
     const uint32_t d_s = dlo(smem_u32(smem + L::S), 8192);
     auto all = [&](bool w) { return (bool)__all_sync(0xffffffffu, w); };
 #pragma unroll 1
-    for (c = 0; c < nch; ++c) {
+    for (int tails = 0; w.chunk(p, order); ++c) {
       const uint32_t st = smem_u32(smem + (c & 1) * L::STAGE);
       const uint32_t d_c = dlo(st + L::C, 16), d_b = dlo(st + L::B, 16), d_x = dlo(st + L::X, 8192);
-      ok = mbar_wait_quiet(&bar[FULL0 + (c & 1)], (c >> 1) & 1) && (c == 0 || mbar_wait_quiet(&bar[GFREE], (c - 1) & 1)) && (len_of(c) == Q || mbar_wait_quiet(&bar[TAIL], 0));
+      ok = mbar_wait_quiet(&bar[FULL0 + (c & 1)], (c >> 1) & 1) && (c == 0 || mbar_wait_quiet(&bar[GFREE], (c - 1) & 1)) && (w.len() == Q || mbar_wait_quiet(&bar[TAIL], tails & 1));
       if (!(ok = all(ok))) break;
+      tails += w.len() < Q;
       tc::fence_after();
 #pragma unroll
       for (uint32_t ks = 0; ks < 8; ++ks) {
@@ -580,7 +636,7 @@ __global__ void __launch_bounds__(896, 1) ssm_tc_kernel(const __grid_constant__ 
     const uint32_t leader = elect();
     const uint32_t d_w = dlo(smem_u32(smem + L::WX), 16384);
 #pragma unroll 1
-    for (c = 0; c < nch; ++c) {
+    for (; w.chunk(p, order); ++c) {
       const uint32_t d_b = dlo(smem_u32(smem + (c & 1) * L::STAGE + L::B), 16384);
       ok = mbar_wait_quiet(&bar[FULL0 + (c & 1)], (c >> 1) & 1) && (c == 0 || mbar_wait_quiet(&bar[DSFREE], (c - 1) & 1));
 #pragma unroll
@@ -871,29 +927,38 @@ cudaError_t launch_ssm_fwd_tc(const SsmParams &s, int nseg, void *workspace, cud
                   !map_rows(fn, &p.tm_c, s.c, rows, (long long)s.G * SSM_N, s.ldc) ||
                   !map_rows(fn, &p.tm_y, s.y, rows, (long long)s.H * s.P, (long long)s.H * s.P)))
     return cudaErrorInvalidValue;
-  if ((size_t)s.n_seqs * nseg * U > 0x7fffffffu) return cudaErrorInvalidConfiguration;
+  if ((size_t)s.n_seqs * nseg * U > 0x7fffffffu / 2) return cudaErrorInvalidConfiguration;
+  p.items = (unsigned)((size_t)s.n_seqs * nseg * U);
   const size_t items = nseg > 1 ? (size_t)s.n_seqs * (nseg - 1) * U : 0;
   p.seg_state = static_cast<float *>(workspace);
   p.seg_decay = p.seg_state + items * SSM_N * SSM_COLS;
   // once per host thread and device: the kernels' shared memory
   static thread_local int ready = -1;
-  int dev = 0;
+  int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess && ready != dev) {
-    e = cudaFuncSetAttribute(ssm_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SsmSmem::BYTES);
+    e = cudaFuncSetAttribute(ssm_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SsmSmem::BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(ssm_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SsmSmem::BYTES);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(ssm_states_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, StSmem::BYTES);
     if (e == cudaSuccess) ready = dev;
   }
   if (e != cudaSuccess) return e;
+  // Short items: a CTA stays and goes on into the next one, so that its loads, state and first products come under the last one's end.
+  // 64 sequences of 128 tokens x 96 heads 389 us with a CTA each, 235 so; 32 of 512 326 and 278; 16 of 1024 257 and 239; 4 of 4096 214
+  // and 220 (the dealing out is fixed, where single CTAs go to whichever SM is free: eight from 0 to 5501 tokens 191 and 205).
+  const bool many = p.items > (unsigned)sms && s.T < (long long)12 * Q * s.n_seqs * nseg;
+  const unsigned ctas = many ? (unsigned)sms : p.items;
+  const auto kernel = many ? ssm_tc_kernel<true> : ssm_tc_kernel<false>;
   if (nseg > 1) {
     ssm_states_kernel<<<(unsigned)items, 608, StSmem::BYTES, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     e = launch_under(ssm_fold_kernel, dim3((unsigned)(s.n_seqs * U), SSM_N * SSM_COLS / 1024), 256, 0, st, p);
     if (e != cudaSuccess) return e;
-    return launch_under(ssm_tc_kernel, dim3((unsigned)((size_t)s.n_seqs * nseg * U)), 896, SsmSmem::BYTES, st, p);
+    return launch_under(kernel, dim3(ctas), 896, SsmSmem::BYTES, st, p);
   }
-  ssm_tc_kernel<<<(unsigned)((size_t)s.n_seqs * U), 896, SsmSmem::BYTES, st>>>(p);
+  kernel<<<ctas, 896, SsmSmem::BYTES, st>>>(p);
   return cudaGetLastError();
 }
 

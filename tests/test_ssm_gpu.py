@@ -406,3 +406,22 @@ def test_long_sums_keep_fp32(kda):
     for h in (0, 17, 39):
         want = b[:, 0].double().t() @ (w[:, h, None] * x[:, h].double())
         assert ref.rel(hT[0, h], want) <= 4e-6
+
+
+@pytest.mark.parametrize("n,H,P,h0", [(90, 4, 64, True), (45, 3, 128, True), (270, 1, 64, False)])
+def test_many_short_prompts(kda, n, H, P, h0):
+    # more (sequence, head) pairs than SMs, of a chunk or two: CTAs go on from one to the next, past empty ones and short last chunks
+    gen = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, 300, (n,), generator=gen).tolist()
+    lens[3] = lens[4] = lens[n - 1] = 0
+    lens[5], lens[6], lens[7] = 1, 128, 256
+    check(kda, lens, H, 1, P, "bf16", seed=n, h0=h0)
+
+
+def test_many_short_prompts_twice(kda):
+    lens = [129, 1, 127, 0, 64] * 24
+    s = case(lens, 3, 1, 64, "bf16", 12)
+    x, b, c = split(s["rows"].cuda(), 3, 1, 64)
+    call = lambda: kda.ssm_fwd(x, s["dt"].cuda(), s["a"].cuda(), b, c, s["cu"], s["h0"].cuda(), d_skip=s["d_skip"].cuda())
+    (y, hT), (y1, hT1) = call(), call()
+    assert torch.equal(y, y1) and torch.equal(hT, hT1)
