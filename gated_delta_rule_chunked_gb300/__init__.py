@@ -557,7 +557,10 @@ def draft_verify(p, q, draft, u, noise, draft_len=None):
     [N, L] fp32 uniforms in [0, 1), noise [N, V] fp32 Exp(1) variates, draft_len [N] optional
     lengths. Draft j stands while u q(x) < p(x); the next token wins the race r / noise over
     r = max(p - q, 0) after a rejection, r = p after the last draft (see include/kda.h).
-    accept_len and first_slot go straight into kda_step / conv_step / ssm_step.
+    kda_step / conv_step / ssm_step then commit the accepted drafts either with ``accept_len``
+    alone (slot j holds draft j) or with ``first_slot`` alone (the accepted drafts at the end of
+    L slots, draft j in slot first_slot + j). Not with both: accept_len counts from slot 0, so
+    only slots first_slot .. accept_len - 1 would be committed.
     """
     lib = library()
     if p.dim() != 3 or not p.is_cuda:

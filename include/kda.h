@@ -455,8 +455,14 @@ size_t kda_ssm_step_workspace_size(const kda_ssm_step_args *args);
  *    when every draft stood. noise holds Exp(1) variates, which makes this a draw from r / sum r.
  *    Entries that are not positive, or NaN, never win; if none of r is positive, p[i, a] takes
  *    its place, and if none of p[i, a] is positive either, the token is -1.
- * accept_len feeds kda_step / kda_conv_step / kda_ssm_step directly: a replay window of
- * L slots with first_slot = L - accept_len. tokens[i] holds the accepted drafts, the next
+ * The accepted drafts enter the committed states (kda_step, kda_conv_step, kda_ssm_step) through
+ * one of the two outputs, not both:
+ *   - accept_len, where slot j of the call holds draft j: the first accept_len slots are
+ *     committed (first_slot NULL);
+ *   - first_slot, where the accepted drafts stand at the end of L slots, draft j in slot
+ *     first_slot + j: the slots before are padding, and all L are committed (accept_len NULL or L).
+ * The steps count accept_len from slot 0, padding included: given both, a call would commit
+ * the slots first_slot .. accept_len - 1 only. tokens[i] holds the accepted drafts, the next
  * token, then -1.
  */
 typedef struct {

@@ -133,3 +133,77 @@ def test_refusals(kda):
         kda.draft_verify(p[:, :1].contiguous(), None, draft[:, :0].contiguous(), u[:, :0].contiguous(), noise)   # no drafts
     with pytest.raises(TypeError):
         kda.draft_verify(p.double(), q.double(), draft, u, noise)
+
+
+def accepted(kda):
+    """Eight sequences of four drafts: draft_verify's accept_len and first_slot, every count among them."""
+    p, q, draft, _, noise = case(8, 4, 32, "f32", seed=9)
+    u = torch.zeros(8, 4)
+    for i, n in enumerate((0, 1, 2, 3, 4, 2, 1, 4)):
+        if n < 4:
+            p[i, n, draft[i, n]] = 0.0                                     # draft n falls
+    accept, first, _ = kda.draft_verify(p.cuda(), q.cuda(), draft.cuda(), u.cuda(), noise.cuda())
+    assert accept.tolist() == [0, 1, 2, 3, 4, 2, 1, 4]
+    return accept, first
+
+
+def commit(kda, op, rows, state, accept=None, first=None):
+    """One call of a recurrent step over `rows` (slots on axis 1); the states after it."""
+    state = [t.clone() for t in state]
+    if op == "kda":
+        kda.kda_step(*rows, state[0], accept, scale=128 ** -0.5, first_slot=first)
+    elif op == "conv":
+        kda.conv_step(rows[0], rows[1][0, 0], None, state[0], accept, first_slot=first)
+    else:
+        kda.ssm_step(rows[0], rows[1], -torch.ones(2, device="cuda"), rows[2][0, 0], None, state[1], state[0], accept, first_slot=first)
+    return state
+
+
+def step_inputs(op):
+    """Rows [8, 4, ...] of fp32 inputs (a weight is one for all slots) and the states of eight sequences."""
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    if op == "kda":
+        return [r(8, 4, 2, 128), r(8, 4, 2, 128), r(8, 4, 2, 128), torch.sigmoid(r(8, 4, 2)), -torch.rand(8, 4, 2, 128, device="cuda", generator=gen)], \
+            [r(8, 2, 128, 128)]
+    channels = 64 if op == "conv" else 2 * 64 + 256
+    weight = r(channels, 4)[None, None].expand(8, 4, -1, -1)
+    if op == "conv":
+        return [r(8, 4, channels), weight], [r(8, 3, channels)]
+    return [r(8, 4, channels), r(8, 4, 2), weight], [r(8, 2, 128, 64), r(8, 3, channels)]
+
+
+@pytest.mark.parametrize("by", ["accept_len", "first_slot"])
+@pytest.mark.parametrize("op", ["kda", "conv", "ssm"])
+def test_accepted_drafts_reach_the_states(kda, op, by):
+    """Either output of draft_verify, as documented, commits exactly the accepted prefix: the states are those of a call over that
+    prefix alone. fp32 sums of at most 128 products over at most 4 tokens, twice: 2 * 4 * 128 * 2^-24 < 1e-4 of the largest value; the
+    convolution's state holds copies."""
+    accept, first = accepted(kda)
+    rows, state = step_inputs(op)
+    if by == "accept_len":
+        got = commit(kda, op, rows, state, accept=accept)
+    else:                                                                  # draft j moves to slot first_slot + j
+        moved = [torch.full_like(t, 7.0) if t.stride(0) else t for t in rows]   # padding is not read
+        for new, t in zip(moved, rows):
+            for i, n in enumerate(accept.tolist()):
+                if t.stride(0):
+                    new[i, 4 - n:] = t[i, :n]
+        got = commit(kda, op, moved, state, first=first)
+    for i, n in enumerate(accept.tolist()):
+        before = [t[i:i + 1] for t in state]
+        want = commit(kda, op, [t[i:i + 1, :n].contiguous() if t.stride(0) else t[i:i + 1, :n] for t in rows], before) if n else before
+        for g, w in zip(got, want):
+            exact = n == 0 or g.dim() == 3
+            assert torch.equal(g[i:i + 1], w) if exact else ref.rel(g[i:i + 1], w) <= 1e-4
+
+
+@pytest.mark.parametrize("op", ["kda", "conv", "ssm"])
+def test_both_outputs_together_commit_less(kda, op):
+    """accept_len counts from slot 0: with first_slot = L - accept_len beside it, up to half of the drafts commit nothing."""
+    accept, first = accepted(kda)
+    rows, state = step_inputs(op)
+    got = commit(kda, op, rows, state, accept=accept, first=first)
+    for i, n in enumerate(accept.tolist()):
+        if 2 * n <= 4:
+            assert all(torch.equal(g[i], s[i]) for g, s in zip(got, state))
