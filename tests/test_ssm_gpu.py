@@ -425,3 +425,18 @@ def test_many_short_prompts_twice(kda):
     call = lambda: kda.ssm_fwd(x, s["dt"].cuda(), s["a"].cuda(), b, c, s["cu"], s["h0"].cuda(), d_skip=s["d_skip"].cuda())
     (y, hT), (y1, hT1) = call(), call()
     assert torch.equal(y, y1) and torch.equal(hT, hT1)
+
+
+def test_step_activation_in_fp32_entry_by_entry(kda):
+    """With zero B rows and states, one tap of one and d_skip = 1, y is silu(x). In fp32 z / (1 + e^-z): the exponential within a unit in
+    the last place (2^-23), the sum and the quotient rounded (2^-24 each): 2^-22 = 2.4e-7 of every entry, at any z with a finite e^-z."""
+    H, P, G = 4, 64, 1
+    z = torch.linspace(-85.0, 85.0, 40 * 8 * H * P).view(40, 8, H * P).cuda()
+    xbc = torch.zeros(40, 8, H * P + 256, device="cuda")
+    xbc[..., :H * P] = z
+    C = H * P + 256
+    y = kda.ssm_step(xbc, torch.zeros(40, 8, H).cuda(), -torch.ones(H).cuda(), torch.ones(C, 1).cuda(), None, None,
+                     torch.zeros(40, H, 128, P).cuda(), d_skip=torch.ones(H).cuda())
+    want = z.double() / (1.0 + torch.exp(-z.double()))
+    err = (y.view_as(z).double() - want).abs() / want.abs()
+    assert err.max().item() <= 2.5e-7
