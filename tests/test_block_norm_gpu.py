@@ -212,3 +212,26 @@ def test_sizes_in_turn(kda, io):
     # the sizes share kernels but not their shared memory: small ones between large ones change nothing
     for dim in (7168, 2056, 16384, 264, 7168, 16384, 128, 2056):
         check(kda, 5, dim, io, dim, **ALL)
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+@pytest.mark.parametrize("dim", [128, 264, 1544, 2056])
+def test_gate_in_fp32_entry_by_entry(kda, act, dim):
+    """Without norms and sums out = u act(z), du = D act(z) and dgate = D u act'(z), entry by entry. In units of 2^-24 of a value: the
+    exponential 2, the sum and the reciprocal 1 each, so 4 of the sigmoid s, 5 of g = z s, and 6 of each product with them. The
+    slopes s + g - g s and s - s s end 12 off the sum of their terms' sizes, counting the products with D and u. Half a unit is
+    left for the second order."""
+    gen = torch.Generator().manual_seed(dim)
+    rows = 50
+    z = torch.linspace(-85.0, 85.0, rows * dim)[torch.randperm(rows * dim, generator=gen)].view(rows, dim)
+    u, D = (torch.rand(rows, dim, generator=gen) + 0.5 for _ in range(2))
+    out, _, stats = kda.block_norm_fwd(u.cuda(), None, gate=z.cuda(), gate_act=act)
+    back = kda.block_norm_bwd(u.cuda(), None, stats, D.cuda(), gate=z.cuda(), gate_act=act)
+    u, z, D = u.double(), z.double(), D.double()
+    s = 1.0 / (1.0 + torch.exp(-z))
+    g = s if act == "sigmoid" else z * s
+    slope = s * (1.0 - s) if act == "sigmoid" else s + g * (1.0 - s)
+    size = s + s * s if act == "sigmoid" else s + g.abs() + g.abs() * s
+    errs = {name: ((got.cpu().double() - want).abs() / size).max().item() * 2 ** 24 for name, got, want, size in (
+        ("out", out, u * g, u * g.abs()), ("du", back["du"], D * g, D * g.abs()), ("dgate", back["dgate"], D * u * slope, D * u * size))}
+    assert errs["out"] <= 6.5 and errs["du"] <= 6.5 and errs["dgate"] <= 12.5, errs
