@@ -137,7 +137,7 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo) { return (uint64_t)(64u | 
 // Byte offset of 16-byte chunk k of row r in a [rows][64] bf16 tile with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t row_chunk(int r, int k) { return (uint32_t)(r * 128 + ((k ^ (r & 7)) << 4)); }
 
-// The sequences by falling length, at most MOST_SORTED.
+// The sequences by falling length, at most MOST_SORTED. The scratch is where a bulk copy lands next.
 constexpr int MOST_SORTED = 256;
 __device__ __forceinline__ void sort_longest(const int *cu, int n_seqs, int *scratch, uint16_t *order) {
   const int t = threadIdx.x;
@@ -149,6 +149,7 @@ __device__ __forceinline__ void sort_longest(const int *cu, int n_seqs, int *scr
     for (int j = 0; j < n_seqs; ++j) rank += scratch[j] > len || (scratch[j] == len && j < t);
     order[rank] = (uint16_t)t;
   }
+  fence_proxy_async();   // the lengths, before that copy
   __syncthreads();
 }
 // One item of the launch: the token a chunk before its first, its chunks, its unit, and sequence | segment << 16 | the last chunk's tokens << 20.

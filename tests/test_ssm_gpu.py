@@ -440,3 +440,27 @@ def test_step_activation_in_fp32_entry_by_entry(kda):
     want = z.double() / (1.0 + torch.exp(-z.double()))
     err = (y.view_as(z).double() - want).abs() / want.abs()
     assert err.max().item() <= 2.5e-7
+
+
+@pytest.mark.parametrize("n,H", [(6, 2), (200, 1), (60, 3), (256, 2)])
+def test_packed_prompts_between_rows_of_nobody(kda, n, H):
+    """Sequences taken by length, one CTA each or going on from one to the next: the lengths are put in order in the shared memory where
+    the first tile arrives. The rows before the first and after the last sequence are not finite and stay out; twenty calls
+    give the same bits."""
+    gen = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, 280, (n,), generator=gen).tolist()
+    lens[0], lens[n // 2], lens[n - 1] = 130, 0, 3
+    before, after, T = 77, 150, sum(lens)
+    s = case([before] + lens + [after], H, 1, 64, "bf16", 13)
+    rows = s["rows"].clone()
+    rows[:before], rows[before + T:] = float("nan"), float("inf")
+    cu, h0 = s["cu"][1:-1].cuda(), s["h0"][1:-1].cuda()
+    x, b, c = split(rows.cuda(), H, 1, 64)
+    call = lambda: kda.ssm_fwd(x, s["dt"].cuda(), s["a"].cuda(), b, c, cu, h0, d_skip=s["d_skip"].cuda())
+    y, hT = call()
+    inside = slice(before, before + T)
+    y_ref, h_ref = ref.scan(x[inside], s["dt"][inside], s["a"], b[inside], c[inside], lens, h0, s["d_skip"])
+    assert ref.rel(y[inside].float(), y_ref) <= TOL["bf16"] and ref.rel(hT, h_ref) <= TOL["f32"]
+    for _ in range(20):
+        y1, hT1 = call()
+        assert torch.equal(y[inside], y1[inside]) and torch.equal(hT, hT1)
