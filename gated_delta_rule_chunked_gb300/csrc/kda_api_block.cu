@@ -44,8 +44,8 @@ kda_status check_ssm(const kda_ssm_args *a, const char *who) {
   if (a->n_seqs < 0 || a->n_seqs > 65535 || a->total_tokens < 0 || a->total_tokens > 0x7fffffffLL)
     return fail(KDA_ERR_INVALID_ARG, who, "need 0 <= n_seqs <= 65535 and 0 <= total_tokens < 2^31");
   if (a->n_seqs == 0 && a->total_tokens > 0) return fail(KDA_ERR_INVALID_ARG, who, "tokens without sequences");
-  if ((int64_t)a->n_seqs * a->heads * (a->head_dim / kda::SSM_COLS) > 0x7fffffffLL)
-    return fail(KDA_ERR_UNSUPPORTED, who, "n_seqs * heads * head_dim / 64 must be below 2^31");
+  if ((int64_t)a->n_seqs * a->heads * (a->head_dim / kda::SSM_COLS) >= (a->io_dtype == KDA_F32 ? 1LL << 31 : kda::SSM_TC_ITEMS))
+    return fail(KDA_ERR_UNSUPPORTED, who, "n_seqs * heads * head_dim / 64 must be below 2^30 (fp32 I/O: 2^31)");
   if (!a->cu_seqlens && a->n_seqs > 0 && a->total_tokens % a->n_seqs != 0)
     return fail(KDA_ERR_INVALID_ARG, who, "without cu_seqlens total_tokens must divide into n_seqs equal sequences");
   if (!fine(a->cu_seqlens, 4) || !fine(a->dev_status, 4)) return fail(KDA_ERR_INVALID_ARG, who, "an int32 array is misaligned");

@@ -277,6 +277,7 @@ struct SsmTcParams {
   unsigned items;     // sequences x segments x units
   float *seg_state, *seg_decay;
 };
+constexpr long long SSM_TC_ITEMS = 1LL << 30;   // items stay below: a CTA's next one is a round past its last, in 32 bits
 int ssm_segments(int n_seqs, long long T, int units);
 size_t ssm_segment_bytes(int n_seqs, int units, int nseg);
 cudaError_t launch_ssm_fwd_tc(const SsmParams &p, int nseg, void *workspace, cudaStream_t s);

@@ -901,7 +901,7 @@ int ssm_segments(int n_seqs, long long T, int units) {
   auto waves = [&](long long k) { return (double)(((long long)n_seqs * units * k + sms - 1) / sms); };
   int best = 1;
   double cost = (chunks + 2.5) * waves(1) + 2.0;
-  for (int k = 2; k <= MOST_SEGS && k * 2 <= chunks; ++k) {
+  for (int k = 2; k <= MOST_SEGS && k * 2 <= chunks && (long long)n_seqs * units * k < SSM_TC_ITEMS; ++k) {
     const double full = waves(k), states = waves(k - 1);
     const double t = chunks / k * (full + 0.5 * states) + 2.5 * (full + states) + 5.0 + 0.5 * k;
     if (t < cost) cost = t, best = k;
@@ -928,7 +928,6 @@ cudaError_t launch_ssm_fwd_tc(const SsmParams &s, int nseg, void *workspace, cud
                   !map_rows(fn, &p.tm_c, s.c, rows, (long long)s.G * SSM_N, s.ldc) ||
                   !map_rows(fn, &p.tm_y, s.y, rows, (long long)s.H * s.P, (long long)s.H * s.P)))
     return cudaErrorInvalidValue;
-  if ((size_t)s.n_seqs * nseg * U > 0x7fffffffu / 2) return cudaErrorInvalidConfiguration;
   p.items = (unsigned)((size_t)s.n_seqs * nseg * U);
   const size_t items = nseg > 1 ? (size_t)s.n_seqs * (nseg - 1) * U : 0;
   p.seg_state = static_cast<float *>(workspace);

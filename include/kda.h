@@ -378,6 +378,7 @@ kda_status kda_conv_step(const kda_conv_step_args *args, cudaStream_t stream);
  * usually the output of kda_conv_fwd, side by side in one row of H * head_dim +
  * 2 * groups * d_state channels, and are read in place through their row strides.
  *  - d_state = 128; head_dim 64 or 128; groups divides heads; a <= 0 is expected.
+ *  - n_seqs * heads * head_dim / 64 < 2^30 (2^31 with fp32 I/O), else KDA_ERR_UNSUPPORTED.
  *  - Row strides (ld*, in elements) must be multiples of 8 and at least the row's width.
  *  - Inputs are finite. A sequence's outputs depend on that sequence's rows only; rows outside every
  *    sequence are left as they are. y and hT overlap no input.

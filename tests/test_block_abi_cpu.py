@@ -64,6 +64,19 @@ def test_ssm_validation(lib, over, status):
     assert lib.kda_last_error().startswith(b"kda_ssm_fwd: ")
 
 
+@pytest.mark.parametrize("io", [0, 1])
+def test_ssm_item_limit(lib, io):
+    """What the launch cannot number is refused with the other arguments, not as a CUDA error."""
+    over = dict(io_dtype=io, n_seqs=32768, total_tokens=0, heads=65536, head_dim=64, ldx=65536 * 64)     # 2^31 items
+    few = dict(over, n_seqs=16383, a=None)                                                               # just below 2^30
+    if io == 0:
+        over["n_seqs"] = 16384                                                                           # 2^30
+    assert lib.kda_ssm_fwd(C.byref(ssm(**over)), None) == UNSUPPORTED
+    assert b"must be below 2^30" in lib.kda_last_error()
+    assert lib.kda_ssm_fwd_workspace_size(C.byref(ssm(**over))) == 0
+    assert lib.kda_ssm_fwd(C.byref(ssm(**few)), None) == INVALID and b"a is NULL" in lib.kda_last_error()      # past that check
+
+
 def step(**over):
     from gated_delta_rule_chunked_gb300 import _lib
     a = _lib.SsmStepArgs()
