@@ -429,6 +429,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream_of(device) -> int:
+    """The current stream of ``device``, which has to be the current device: the library launches there."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
     return _raw_stream(device.index) if _raw_stream is not None else _stream(device)
 
 

@@ -148,3 +148,14 @@ def test_norm_validation(lib, over, status):
 def test_null_arguments(lib):
     for name in ("kda_ssm_fwd", "kda_ssm_step", "kda_draft_verify", "kda_block_norm_fwd", "kda_block_norm_bwd"):
         assert getattr(lib, name)(None, None) == INVALID
+
+
+def test_tensors_on_another_device_are_refused(monkeypatch):
+    """The library launches on the current device: a stream is only handed out for tensors that live there."""
+    import torch
+    import gated_delta_rule_chunked_gb300 as kda
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(kda, "_raw_stream", lambda index: 40 + index)
+    assert kda._stream_of(torch.device("cuda", 0)) == 40
+    with pytest.raises(ValueError, match="cuda:1"):
+        kda._stream_of(torch.device("cuda", 1))
