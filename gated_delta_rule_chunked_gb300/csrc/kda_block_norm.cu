@@ -408,7 +408,7 @@ __device__ __forceinline__ void take_sums(float (&s)[3], const float *red, uint3
 
 // Long rows: a cluster of CTAs per row, each with 8 columns per thread. Persistent: cluster k of K takes
 // rows k, k + K, ...; the row's slices of the inputs arrive by bulk copies into a ring of p.stages buffers
-// (a row's buffer serves both its halves). A row's sums travel while the next row's first half is
+// (a row's buffer serves both its halves, and is refilled at the end of the next row's turn). A row's sums travel while the next row's first half is
 // computed. The two arrays of sums alternate: a CTA's parts of row i + 2 are sent after it has all parts
 // of row i + 1, and a warp sends those after it has read the sums of row i.
 template <typename IO, int GATE, bool FULL>
@@ -442,10 +442,10 @@ __global__ void __launch_bounds__(256, 2) block_norm_bwd_kernel(BlockNormParams 
     for (int i = 0; i < 5; ++i)
       if (src[i]) bulk_g2s(bn_ring + b * buffer + i * stride, static_cast<const IO *>(src[i]) + r * p.dim + (size_t)vbeg * 8, slice, &bar[2 + b]);
   };
-  long long ahead = k0;   // the next row to ask for; two buffers are the current row's and the previous one's
+  long long ahead = k0;   // the next row to ask for: at the end of a turn the previous row's buffer is free, the current row's is not
   if (tid == 0)
-    for (int i = 0; i < p.stages - 2 && ahead < p.rows; ++i, ahead += K) issue(ahead, i);
-  int fill = p.stages - 2;
+    for (int i = 0; i < p.stages - 1 && ahead < p.rows; ++i, ahead += K) issue(ahead, i);
+  int fill = p.stages - 1;
   BwdCols<IO> col(p, c);
   BwdRow<IO, GATE, FULL> prev;
   bool ok = true;
@@ -601,7 +601,9 @@ Kernel bwd_fn(int lpr, int gate, bool full, bool f32) {
 // The backward's launch. Long rows: as few CTAs per row (of 1 to 8) as keep nearly the most columns on an SM that any count does
 // (bf16: 5120 columns in 4 of 160 threads 5.2 TB/s, in 4 that fill two thirds of an SM 4.1; 6144 in 3 of 256 5.2, in 4 of 192
 // 4.9; 7168 in 4 of 224 5.0, in 7 of 128, a seventh more, 4.9). In fp32 a CTA takes up to 128 threads, whose rows leave room for others
-// (2048 columns in 2 of 128 5.4 TB/s, in one of 256 3.7). Three to six buffers, as many as leave room for the SM's CTAs. The
+// (2048 columns in 3 of 96, which the rule takes, 6.2 TB/s, in 2 of 128 6.3, in one of 256 5.9). Three to six buffers, as many as leave
+// room for the SM's CTAs; all but the current row's are full or being filled (with one more left empty, as before, fp32 rows of 1544
+// columns 5.1 instead of 6.2 TB/s, of 8192 4.6 and 6.5; bf16, with five or six buffers, the same). The
 // count of CTAs sizes the workspace, so it goes by the sizes alone: the gate's kernels are taken to hold as many at once as the SiLU's.
 constexpr int BWD_RING = 216 * 1024;   // the rings of an SM's CTAs together
 struct BwdLaunch {

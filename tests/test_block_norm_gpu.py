@@ -235,3 +235,10 @@ def test_gate_in_fp32_entry_by_entry(kda, act, dim):
     errs = {name: ((got.cpu().double() - want).abs() / size).max().item() * 2 ** 24 for name, got, want, size in (
         ("out", out, u * g, u * g.abs()), ("du", back["du"], D * g, D * g.abs()), ("dgate", back["dgate"], D * u * slope, D * u * size))}
     assert errs["out"] <= 6.5 and errs["du"] <= 6.5 and errs["dgate"] <= 12.5, errs
+
+
+@pytest.mark.parametrize("io,rows,dim", [("f32", 2900, 1544), ("f32", 2100, 2048), ("f32", 700, 8192), ("bf16", 1500, 7168), ("f32", 457, 16384),
+                                         ("bf16", 2600, 1032)])
+def test_rows_round_the_ring(kda, io, rows, dim):
+    """Rings of three buffers (fp32 of 1544, 2048 and 8192 columns) and more, each filled several times over."""
+    check(kda, rows, dim, io, dim, **ALL)
