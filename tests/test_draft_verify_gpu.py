@@ -207,3 +207,22 @@ def test_both_outputs_together_commit_less(kda, op):
     for i, n in enumerate(accept.tolist()):
         if 2 * n <= 4:
             assert all(torch.equal(g[i], s[i]) for g, s in zip(got, state))
+
+
+@pytest.mark.parametrize("V", [1000, 1001])
+def test_captured_in_a_graph(kda, V):
+    """Captured on one set of inputs and replayed on others in their place."""
+    first, second = ([cuda(t) for t in case(9, 3, V, "f32", seed=s)] for s in (21, 22))
+    args = [t.clone() for t in first]
+    kda.draft_verify(*args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = kda.draft_verify(*args)
+    for values in (first, second):
+        for a, v in zip(args, values):
+            a.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = ref.verify(*[t.cpu() for t in values])
+        assert all((g.cpu().numpy() == w).all() for g, w in zip(got, want))
