@@ -5,7 +5,7 @@ A toy model: embedding, one block, unembedding. The block is
     normed = RMS norm of the residual stream        block_norm_fwd (norm before the block)
     xbc    = normed W_in                            raw rows [x | B | C]
     prompt: conv_fwd, ssm_fwd                       drafts: ssm_step (convolution and scan in one call)
-    u      = y * silu(z), RMS-normed per head       block_norm_fwd (output norm of the core)
+    u      = RMS norm of y per head, times silu(z)  block_norm_fwd (output norm of the core)
     out    = residual + scale * RMS norm(u W_out)   block_norm_fwd (norm after the block, and before the next)
 
 Decoding drafts L tokens at a time (here from the model's own distribution, disturbed), verifies them in one

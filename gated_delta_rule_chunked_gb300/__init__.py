@@ -481,7 +481,8 @@ def ssm_fwd(x, dt, a, b, c, cu_seqlens=None, h0=None, *, d_skip=None, dt_bias=No
     x [T, H, P] (P = 64 or 128), b and c [T, G, 128] in bfloat16 or float32 may be views into one
     row, such as conv_fwd's output split into [x | B | C]; dt [T, H], a [H], d_skip [H], dt_bias
     [H] are fp32, and the states h0, hT [N, H, 128, P] fp32 (row = state channel). Per token and
-    head: h = softplus(dt + dt_bias), S = exp(h a) S + h B x^T, y = S^T C + d_skip x.
+    head: h = softplus(dt + dt_bias), S = exp(h a) S + h B x^T, y = S^T C + d_skip x. For serving:
+    there is no backward, and the results carry no gradient whatever the inputs require.
     """
     lib = library()
     if x.dim() != 3 or not x.is_cuda or b.dim() != 3:

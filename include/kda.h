@@ -374,6 +374,7 @@ kda_status kda_conv_step(const kda_conv_step_args *args, cudaStream_t stream);
  * (row n = state channel, column p = value channel), one scalar decay per head and token:
  *     h_t = softplus(dt_t + dt_bias)   (or dt_t + dt_bias without dt_softplus)
  *     S_t = exp(h_t a) S_{t-1} + h_t B_t x_t^T,      y_t = S_t^T C_t + d_skip x_t
+ * Serving forms only: there is no backward, so the scan cannot be trained through this library.
  * B and C are shared by the heads / groups consecutive heads of a group. x, B and C are
  * usually the output of kda_conv_fwd, side by side in one row of H * head_dim +
  * 2 * groups * d_state channels, and are read in place through their row strides.
@@ -386,7 +387,8 @@ kda_status kda_conv_step(const kda_conv_step_args *args, cudaStream_t stream);
  * decays and all sums are fp32. The state update splits its fp32 factor into three bf16 terms
  * (error 2^-24 of a term). The decay-weighted scores of a chunk, and the copy of the state that a
  * chunk's outputs read, are rounded to bf16 once, which costs y about as much as its own rounding
- * to bf16. fp32 I/O runs in fp32 on the CUDA cores. Sequences with few heads run in segments in
+ * to bf16 (2^-9 of the root of the sum of its squared terms: more than that rounding where they
+ * cancel). fp32 I/O runs in fp32 on the CUDA cores. Sequences with few heads run in segments in
  * either type, through a workspace; without one the size is 0.
  */
 typedef struct {
@@ -419,7 +421,8 @@ size_t kda_ssm_fwd_workspace_size(const kda_ssm_args *args);
  * slots per sequence, [x | B | C] side by side before the convolution, with the slot
  * conventions of kda_step and kda_conv_step (state_indices into pools of n_slots states; slots
  * before first_slot[i] are padding; both states advance through accept_len[i] slots). The
- * convolution's outputs stay in fp32 between the two. */
+ * convolution's outputs stay in fp32 between the two; its SiLU is within 2^-22 of a value with fp32
+ * I/O, and within about (4 + |z|) 2^-24 with bf16 I/O. */
 typedef struct {
     int32_t n_seqs, steps;     /* N in 0..65535, L in 1..8                               */
     int32_t heads, groups, head_dim, d_state;   /* as in kda_ssm_args                    */
@@ -490,7 +493,8 @@ kda_status kda_draft_verify(const kda_draft_verify_args *args, cudaStream_t stre
  *     m   *= act(gate)                              (gate optional: sigmoid or SiLU)
  *     out  = residual + scale m                     (residual, scale optional)
  *     normed = w_pre out / sqrt(mean(out^2) + eps)  (w_pre optional)
- * normed is formed from the unrounded out. Rows are tokens, or (token, head) pairs for the
+ * The gate comes after the norm; a norm of the gated u is not offered. The gate's exponential is
+ * within 2^-22 of a value with fp32 I/O, and within (4 + |z|) 2^-24 with bf16 I/O. normed is formed from the unrounded out. Rows are tokens, or (token, head) pairs for the
  * output norm of a recurrent core.
  */
 typedef enum { KDA_GATE_SIGMOID = 0, KDA_GATE_SILU = 1 } kda_gate;
