@@ -11,7 +11,9 @@
 // Memory-bound: every tensor is read and written once, everything in between is fp32 registers. In bf16 the forward
 // moves 2.35 GB at 32768 x 7168 in 0.356 ms (6.6 TB/s, 97% of a copy) and 0.30 GB at 393216 x 128 in 51 us (5.9 TB/s); the
 // backward moves 1.88 GB at 16384 x 7168 in 0.367 ms (5.1 TB/s): it keeps 14 warps on an SM, whose registers the sums over rows
-// and the column vectors fill, and issues in 55% of the slots.
+// and the column vectors fill, and issues in 55% of the slots. In fp32 8192 x 7168 take 174 us forward (6.7 TB/s) and 295 us backward (6.4
+// TB/s). The backward of short rows moves 0.50 GB at 393216 x 128 in bf16 in 112 us (4.5 TB/s): a thread asks for its next row only when it
+// has stored the current one, at 16 warps an SM.
 // Forward: a row is owned by LPR lanes of a warp (short rows) or by a whole CTA (LPR = 0), each thread
 // holding VPT vectors of 8 elements.
 #include "kda_common.cuh"
@@ -602,7 +604,7 @@ Kernel bwd_fn(int lpr, int gate, bool full, bool f32) {
 // (bf16: 5120 columns in 4 of 160 threads 5.2 TB/s, in 4 that fill two thirds of an SM 4.1; 6144 in 3 of 256 5.2, in 4 of 192
 // 4.9; 7168 in 4 of 224 5.0, in 7 of 128, a seventh more, 4.9). In fp32 a CTA takes up to 128 threads, whose rows leave room for others
 // (2048 columns in 3 of 96, which the rule takes, 6.2 TB/s, in 2 of 128 6.3, in one of 256 5.9). Three to six buffers, as many as leave
-// room for the SM's CTAs; all but the current row's are full or being filled (with one more left empty, as before, fp32 rows of 1544
+// room for the SM's CTAs; all but the current row's are full or being filled (with one more left empty fp32 rows of 1544
 // columns 5.1 instead of 6.2 TB/s, of 8192 4.6 and 6.5; bf16, with five or six buffers, the same). The
 // count of CTAs sizes the workspace, so it goes by the sizes alone: the gate's kernels are taken to hold as many at once as the SiLU's.
 constexpr int BWD_RING = 216 * 1024;   // the rings of an SM's CTAs together

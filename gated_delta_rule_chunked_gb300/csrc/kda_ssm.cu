@@ -9,8 +9,8 @@
 // the sums over the row groups meet once per batch of tokens. No product goes through the tensor cores, whose
 // operands would not hold 24 bits. Prompts are bound by the issue of those products and sums (52% of the issue
 // slots at two warps a scheduler; 2048 tokens x 96 heads of 64 in 410 us).
-// Step: bound by reading and writing the 32 KB state (256 sequences x 4 slots x 96 heads of 64, 1.66 GB:
-// 295 us, 5.6 TB/s, when every sequence commits; 258 us at drawn prefixes, of which some commit nothing). The convolution runs as a kernel of
+// Step: bound by reading and writing the 32 KB state (256 sequences x 4 slots x 96 heads of 64: 314 us for 1.67 GB, 5.3
+// TB/s, when every sequence commits; 258 us for 1.38 GB at drawn prefixes, of which a third commit nothing and write no state). The convolution runs as a kernel of
 // its own (its state is shared by every head of a group, so it cannot be advanced in place by the heads'
 // CTAs), and the scan starts under it (programmatic dependent launch): it has its state in
 // registers by the time the convolution's rows are there.

@@ -18,7 +18,7 @@
 // Loops stay rolled: the roles share one instruction cache, and with unrolled bodies every chunk
 // fetched its code from beyond it (32768 tokens x 96 heads of 64 in 1.16 instead of 0.92 ms, before the other steps).
 // Bound by shared memory: a chunk moves 80 KB in and 16 KB out by TMA, w o X, X, Y and S through registers, and
-// the products read 1664 lines of 128 bytes of operands; together about 95% of its cycles, 1.9 us a chunk, with the
+// the products read 1664 lines of 128 bytes of operands; together 90 to 92% of its cycles, 1.9 us a chunk, with the
 // tensor cores 45% and the issue slots 52% busy. 32768 tokens x 96 heads of 64 take 0.486 ms, 2.0 TB/s of inputs and
 // outputs, on the 96 SMs that have a head.
 // Rounding: the products take bf16 operands and add in fp32. X, B, C are bf16 already; M and the

@@ -10,16 +10,17 @@
 // once, and the cluster's winners meet in every CTA through distributed shared memory. The correctly
 // rounded division, which decides ties, is made only for entries that an approximate quotient puts
 // within 2^-20 of the warp's leader or above it.
-// Bound by the bytes of those rows: 256 sequences x 131072 fp32 with three rows each, 403 MB, in 59.6 us, 6.76 TB/s
-// (99.5% of a copy). At one sequence by latency, for which the cluster is wide (6 us, and as much again to launch).
+// Bound by the bytes of those rows: the target's, the noise, and after a rejection the drafter's. 256 sequences x 131072 fp32, of which
+// about half have a draft rejected, 333 MB, in 59.8 us, 5.6 TB/s (82% of a copy): 2048 CTAs in under three waves, each of which starts
+// with dependent loads at the drafted tokens. At one sequence by latency, for which the cluster is wide (6 us, and as much again to launch).
 #include "kda_common.cuh"
 #include "kda_internal.h"
 
 namespace kda {
 namespace {
 
-// 8 CTAs of 256 threads per sequence, five or more on an SM. Compared at 256 sequences x 131072 fp32 where no draft fails (two rows):
-// 50 us; with 512 threads 55 to 74; with 4 CTAs 48 to 58, but 11 instead of 8 us for one sequence.
+// 8 CTAs of 256 threads per sequence, five or more on an SM. Compared at 256 sequences x 131072 fp32 where no draft fails (two rows,
+// 268 MB): 50 us; with 512 threads 55 to 74; with 4 CTAs 48 to 58, but 11 instead of 8 us for one sequence.
 constexpr int VF_T = 256;
 constexpr unsigned VF_CL = 8;
 constexpr int VF_MAXL = 8;
