@@ -100,7 +100,7 @@ __device__ __forceinline__ float reciprocal(float d) {
 }
 // 1 / (1 + e^-z). fp32 rows by expf and the refined reciprocal, to 2^-22 of a value (8192 x 7168 with SiLU:
 // forward 176 -> 178 us, backward 341 -> 353; with a correctly rounded reciprocal 223 and 402). bf16 rows by the hardware's 2^x and reciprocal: the
-// rounding of z log2(e) makes that about (4 + |z|) 2^-24 of a value, 5e-6 at |z| = 85, beside results rounded at 2^-9.
+// rounding of z log2(e) makes that up to (9 + 2.4 |z|) 2^-24 of a value, beside results rounded at 2^-9.
 template <typename IO>
 __device__ __forceinline__ f2 sigmoid(f2 z) {
   if constexpr (sizeof(IO) == 4) {
