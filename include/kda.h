@@ -422,7 +422,7 @@ size_t kda_ssm_fwd_workspace_size(const kda_ssm_args *args);
  * conventions of kda_step and kda_conv_step (state_indices into pools of n_slots states; slots
  * before first_slot[i] are padding; both states advance through accept_len[i] slots). The
  * convolution's outputs stay in fp32 between the two; its SiLU is within 2^-22 of a value with fp32
- * I/O, and within (9 + 2.4 |z|) 2^-24 with bf16 I/O. */
+ * I/O, and within (9 + 2.4 |z|) 2^-24 with bf16 I/O (below z = -87 it may be 0). */
 typedef struct {
     int32_t n_seqs, steps;     /* N in 0..65535, L in 1..8                               */
     int32_t heads, groups, head_dim, d_state;   /* as in kda_ssm_args                    */
@@ -493,9 +493,10 @@ kda_status kda_draft_verify(const kda_draft_verify_args *args, cudaStream_t stre
  *     m   *= act(gate)                              (gate optional: sigmoid or SiLU)
  *     out  = residual + scale m                     (residual, scale optional)
  *     normed = w_pre out / sqrt(mean(out^2) + eps)  (w_pre optional)
- * The gate comes after the norm; a norm of the gated u is not offered. The gate's exponential is
- * within 2^-22 of a value with fp32 I/O, and within (9 + 2.4 |z|) 2^-24 with bf16 I/O. normed is formed from the unrounded out. Rows are tokens, or (token, head) pairs for the
- * output norm of a recurrent core.
+ * The gate comes after the norm; a norm of the gated u is not offered. Its sigmoid is within
+ * 2^-22 of a value with fp32 I/O, and within (9 + 2.4 |z|) 2^-24 with bf16 I/O (below z = -87 it
+ * may be 0). normed is formed from the unrounded out. Rows are tokens, or (token, head) pairs for
+ * the output norm of a recurrent core.
  */
 typedef enum { KDA_GATE_SIGMOID = 0, KDA_GATE_SILU = 1 } kda_gate;
 
